@@ -66,7 +66,7 @@ typedef enum {
   SPECDEC_ERR_NULL = -1,      /* a required pointer is NULL                               */
   SPECDEC_ERR_SHAPE = -2,     /* B < 0, K < 0, K > SPECDEC_MAX_K, V < 1, or                */
                               /* B*(K+1)*ceil(V/8192) >= 2^31                               */
-  SPECDEC_ERR_DTYPE = -3,     /* logits_dtype is not a specdec_dtype                      */
+  SPECDEC_ERR_DTYPE = -3,     /* logits_dtype (a cache's dtype) is not one the call takes */
   SPECDEC_ERR_ALIGN = -4,     /* a tensor base is not aligned to its element size         */
   SPECDEC_ERR_WORKSPACE = -5, /* workspace NULL or smaller than specdec_workspace_size()  */
   SPECDEC_ERR_LAUNCH = -6,    /* a kernel launch or event record failed                   */
@@ -76,7 +76,8 @@ typedef enum {
 
 typedef enum {
   SPECDEC_F32 = 0,            /* IEEE binary32 logits                                     */
-  SPECDEC_BF16 = 1            /* bfloat16 logits (upper 16 bits of a binary32)            */
+  SPECDEC_BF16 = 1,           /* bfloat16 logits (upper 16 bits of a binary32)            */
+  SPECDEC_F16 = 2             /* IEEE binary16: the paged-cache entry points only         */
 } specdec_dtype;
 
 #define SPECDEC_MAX_K 63                  /* drafts per sequence (K+1 rows fit one wave64) */
@@ -356,6 +357,172 @@ specdec_status specdec_plan_k(const int64_t* counters, int32_t n_routes, double 
  * proposals past the new count are simply not verified. */
 specdec_status specdec_apply_k(int32_t* num_draft, const int32_t* route, const int32_t* k_table,
                                int32_t B, int32_t n_routes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The paged key-value cache of a round.  specdec_commit rolls a cache's LENGTHS back; these entry
+ * points work on its contents.  One round of a model over such a cache:
+ *   per layer   specdec_rope_append       rotate q and k of the k_b + 1 new tokens (the last emitted
+ *                                         token, then the drafts) and put k and v into slots
+ *                                         kv_len[b] .. kv_len[b] + k_b
+ *               specdec_paged_attention   each of those tokens attends to every slot up to its own
+ *   per round   specdec_verify            accept_len from the logits
+ *   per layer   specdec_kv_weights        (caches that evict) add the attention weights that the
+ *                                         accepted rows gave each slot
+ *   per round   kv_len[b] += k_b + 1, then specdec_commit (target_kv_len = kv_len) rolls it back; a
+ *               cache that has evicted holds fewer slots than the sequence has tokens, which is what
+ *               the commit rolls back to: its kv_len[b] += accept_len[b] + 1 instead
+ *   per layer   specdec_kv_evict          (caches that evict) keep the heaviest slots
+ * kv_len[b] is the number of slots in use BEFORE the round, the same for every layer, and none of
+ * the per-layer calls changes it.
+ *
+ * Pages.  A sequence's slot j lies in page page_table[b, j / page_size] at place j % page_size;
+ * entries of the table past the used slots are never read as page ids (any value).  A page that
+ * specdec_rope_append, specdec_kv_weights or specdec_kv_evict writes belongs to one sequence of
+ * the batch; pages that are only read may be shared.
+ *
+ * A sequence is invalid in these calls when k_b is outside [0, K], kv_len[b] < 0, kv_len[b] + k_b +
+ * 1 exceeds max_pages * page_size, or a page id of its used slots is outside [0, num_pages).  Its
+ * output rows 0..k_b (all K + 1 if k_b itself is the fault) are NaN, so that the logits computed
+ * from them make specdec_verify report the sequence (accept_len -1), and nothing of the cache is
+ * written for it except where an entry point says otherwise.  Output rows past k_b of a valid
+ * sequence are 0 (their lse -infinity); input rows past k_b are never read as values.
+ *
+ * Element types: bf16, f16 or f32, one for q, k, v, the cache and the outputs.  Scores, softmax
+ * statistics, weights and sums are f32; rotation angles are f64.  Every row (the head_dim elements
+ * of one head) has to lie on a 16-byte boundary: pointers and strides that break that are
+ * SPECDEC_ERR_ALIGN.  The struct itself is HOST memory, read during the call. */
+typedef struct {
+  void* k;                    /* key pool;   row of (page p, place s, head h) at element            */
+  void* v;                    /* value pool; p * page_stride + s * slot_stride + h * head_stride    */
+  int32_t dtype;              /* specdec_dtype                                                     */
+  int32_t num_pages;          /* pages in the pool; num_pages * page_size < 2^31                    */
+  int32_t page_size;          /* slots a page, >= 1                                                */
+  int32_t num_kv_heads;       /* >= 1                                                              */
+  int32_t head_dim;           /* a multiple of 8, 8 .. SPECDEC_MAX_HEAD_DIM                         */
+  int32_t max_pages;          /* entries of a row of page_table; max_pages * page_size < 2^31       */
+  int64_t page_stride;        /* in elements, each >= head_dim (where the count is over 1)          */
+  int64_t slot_stride;
+  int64_t head_stride;
+  const int32_t* page_table;  /* [B, max_pages]                                                    */
+  float* weight;              /* [num_pages, num_kv_heads, page_size] accumulated weights, or NULL  */
+  int32_t* position;          /* the same shape: each slot's token position, or NULL               */
+} specdec_kv_cache;
+
+#define SPECDEC_MAX_HEAD_DIM 256
+
+/* Rotary positions.  Pair i of a head's first rotary_dim elements, (i, i + rotary_dim / 2) or with
+ * interleaved (2 i, 2 i + 1), is turned by position * inv_freq[i] and multiplied by scale:
+ *   a' = scale (a cos t - b sin t),   b' = scale (b cos t + a sin t);
+ * elements from rotary_dim on are copied.  The angle is formed and reduced in f64. */
+typedef struct {
+  const double* inv_freq;     /* DEVICE [rotary_dim / 2] (specdec_rope_frequencies)                 */
+  int32_t rotary_dim;         /* even, 0 .. head_dim (0: nothing is turned, inv_freq may be NULL)   */
+  int32_t interleaved;        /* nonzero: adjacent pairs                                           */
+  float scale;                /* finite; 1 unless the scaling method asks for another              */
+} specdec_rope;
+
+/* Angular frequencies of rotary pairs, HOST arithmetic in f64: inv_freq[i], i < rotary_dim / 2.
+ * f_i = base^(-2 i / rotary_dim) and, for contexts `factor` times longer than original_len,
+ *   SPECDEC_ROPE_PLAIN   f_i;
+ *   SPECDEC_ROPE_LINEAR  f_i / factor (positions interpolated);
+ *   SPECDEC_ROPE_BASE    f_i with base * factor^(rotary_dim / (rotary_dim - 2));
+ *   SPECDEC_ROPE_TURNS   pairs that make at most turns_low turns over original_len are interpolated
+ *                        (f_i / factor), those that make at least turns_high are kept, linearly
+ *                        blended in between by their number of turns original_len f_i / (2 pi).
+ * SPECDEC_ERR_SHAPE: rotary_dim odd or outside [2, SPECDEC_MAX_HEAD_DIM] (BASE: < 4), base <= 1,
+ * factor < 1, an unknown scaling, or for TURNS original_len <= 0 or not 0 <= turns_low < turns_high;
+ * arguments that the method does not use are ignored. */
+#define SPECDEC_ROPE_PLAIN 0
+#define SPECDEC_ROPE_LINEAR 1
+#define SPECDEC_ROPE_BASE 2
+#define SPECDEC_ROPE_TURNS 3
+
+specdec_status specdec_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling,
+                                        double factor, double original_len, double turns_low,
+                                        double turns_high, double* inv_freq);
+
+/* Rotates the new tokens' q and k, and puts k and v into the cache.
+ *
+ * q           [B, K+1, num_q_heads, head_dim]; tokens q_stride elements apart (row (b, i) at
+ *             (b (K+1) + i) q_stride), heads and elements dense.  A fused projection's slices are
+ *             passed without a copy.  k, v [B, K+1, num_kv_heads, head_dim] likewise.
+ * K           any K >= 0 with B * (K+1) < 2^31: a prompt is a round with num_draft = length - 1.
+ * num_draft   [B]    int32 k_b in [0, K].  NULL = K.
+ * kv_len      [B]    int32 slots in use before the round.
+ * first_pos   [B]    int32 position of each sequence's first new token (the following ones count up);
+ *             NULL = kv_len (right until the cache evicts; afterwards seq_len - 1).  A sequence
+ *             whose positions are negative or pass 2^31 - 1 is invalid.
+ * q_out       [B, K+1, num_q_heads, head_dim] dense, out; may be q itself if q is dense.
+ * cache       k, v rows of the new slots are written; also weight (0) and position where given.
+ * A new token whose page id is outside the pool gets a NaN q_out row and writes nothing, the
+ * sequence's other tokens are done.  No workspace. */
+specdec_status specdec_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, int32_t B, int32_t K,
+                                   int32_t num_q_heads, const int32_t* num_draft,
+                                   const int32_t* kv_len, const int32_t* first_pos,
+                                   const specdec_rope* rope, const specdec_kv_cache* cache,
+                                   void* q_out, void* stream);
+
+/* Attention of a round's tokens over the cache (K = 0: one new token a sequence).  For row i of
+ * sequence b and query head h, with g = h / (num_q_heads / num_kv_heads):
+ *   x_j = scale q[b, i, h] . k_j[g],  j = 0 .. kv_len[b] + i;
+ *   lse = log sum_j exp(x_j),   out[b, i, h] = sum_j exp(x_j - lse) v_j[g].
+ * A row whose keys give only scores of -infinity is NaN, as is one that sees a NaN; values in slots
+ * that a row does not see, NaN and infinities included, never reach it.
+ *
+ * q           [B, K+1, num_q_heads, head_dim], tokens q_stride elements apart; 0 <= K <=
+ *             SPECDEC_MAX_K; num_q_heads a multiple of num_kv_heads; scale finite, > 0.
+ * out         [B, K+1, num_q_heads, head_dim] dense.   lse [B, K+1, num_q_heads] f32 or NULL.
+ * workspace   device scratch of >= specdec_paged_attention_workspace_size() bytes, 16-byte aligned,
+ *             no initialisation needed; calls that overlap in time need their own.
+ * The new tokens' own keys and values are read from the cache (specdec_rope_append put them there). */
+size_t specdec_paged_attention_workspace_size(int32_t B, int32_t K, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim);
+
+specdec_status specdec_paged_attention(const void* q, int64_t q_stride, int32_t B, int32_t K,
+                                       int32_t num_q_heads, const int32_t* num_draft,
+                                       const int32_t* kv_len, float scale,
+                                       const specdec_kv_cache* cache, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Adds to cache->weight what the round's accepted rows gave each slot:
+ *   weight_j[g] += sum_{i <= A} sum_{h of g} exp(scale q[b, i, h] . k_j[g] - lse[b, i, h]),
+ *   j <= kv_len[b] + i, with A = accept_len[b]
+ * (row 0 and the A accepted drafts' rows; the rejected drafts' slots are left alone).  q, lse, kv_len
+ * and num_draft are those of the attention call.
+ *
+ * accept_len  [B]    int32 in [0, k_b]; a sequence with another value (-1: invalid) adds nothing.
+ *             NULL = every row 0..k_b counts.
+ * Slots on pages outside the pool are passed over.  cache->weight is required.  No workspace; the
+ * sums are made in a fixed order, without atomics. */
+specdec_status specdec_kv_weights(const void* q, int64_t q_stride, const float* lse, int32_t B,
+                                  int32_t K, int32_t num_q_heads, const int32_t* num_draft,
+                                  const int32_t* accept_len, const int32_t* kv_len, float scale,
+                                  const specdec_kv_cache* cache, void* stream);
+
+/* Evicts slots: of a sequence with L = kv_len[b] > budget slots, every kv head keeps `budget`:
+ * the slots whose position is below keep_first or among the newest keep_last positions (position >
+ * newest - keep_last, newest = the largest position of the L slots), then those of the largest weight
+ * (NaN below every number; ties: the lower slot).  The kept slots from `budget` on move into the
+ * evicted slots below it, the first into the first and so on: k, v, weight and position.  So the
+ * fewest rows move; slots are no longer in order of position (attention does not need it).  Slots
+ * from `budget` on keep their old contents.  A sequence with L <= budget is unchanged.
+ *
+ * kv_len      [B]    int32 slots in use.   1 <= budget, 0 <= keep_first, keep_last, keep_first +
+ *             keep_last <= budget.  (Positions that repeat can protect more than that: of these
+ *             the lower slots are kept.)
+ * new_len     [B] out int32 min(L, budget), or -1 for an invalid sequence (L outside [0, max_pages *
+ *             page_size] or a page id of its slots outside the pool), of which nothing moves; NULL
+ *             = not wanted.  It may be kv_len itself (in the last layer's call).
+ * workspace   device scratch of >= specdec_kv_evict_workspace_size() bytes, 16-byte aligned, no
+ *             initialisation needed; calls that overlap in time need their own.
+ * cache->weight and cache->position are required. */
+size_t specdec_kv_evict_workspace_size(int32_t B, const specdec_kv_cache* cache, int32_t budget);
+
+specdec_status specdec_kv_evict(const specdec_kv_cache* cache, const int32_t* kv_len, int32_t B,
+                                int32_t budget, int32_t keep_first, int32_t keep_last,
+                                int32_t* new_len, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* specdec_status_string(int32_t status);

@@ -12,7 +12,10 @@ from .binding import (SpecdecError, specdec_verify, specdec_verify_greedy, specd
                       specdec_apply_k, specdec_plan_k, telemetry_counters,
                       SPECDEC_PATH_AUTO, SPECDEC_PATH_STREAMING, SPECDEC_PATH_SMALL_VOCAB,
                       SPECDEC_SMALL_V_MAX, SPECDEC_PATH_ONE_LAUNCH, SPECDEC_PATH_QUAD, new_workspace,
-                      specdec_verify_noalloc)
+                      specdec_verify_noalloc, PagedKvCache, specdec_rope_frequencies,
+                      specdec_rope_append, specdec_paged_attention,
+                      specdec_paged_attention_workspace_size, new_paged_attention_workspace,
+                      specdec_kv_weights, specdec_kv_evict, new_kv_evict_workspace)
 
 __all__ = ["SpecdecError", "specdec_verify", "specdec_verify_greedy", "specdec_workspace_size",
            "specdec_status_string", "library_path", "load_library", "inputs_to_device",
@@ -21,4 +24,7 @@ __all__ = ["SpecdecError", "specdec_verify", "specdec_verify_greedy", "specdec_w
            "specdec_plan_k", "telemetry_counters", "SPECDEC_PATH_AUTO", "SPECDEC_PATH_STREAMING",
            "SPECDEC_PATH_SMALL_VOCAB", "SPECDEC_SMALL_V_MAX", "SPECDEC_PATH_ONE_LAUNCH",
            "SPECDEC_PATH_QUAD",
-           "new_workspace", "specdec_verify_noalloc"]
+           "new_workspace", "specdec_verify_noalloc", "PagedKvCache", "specdec_rope_frequencies",
+           "specdec_rope_append", "specdec_paged_attention",
+           "specdec_paged_attention_workspace_size", "new_paged_attention_workspace",
+           "specdec_kv_weights", "specdec_kv_evict", "new_kv_evict_workspace"]

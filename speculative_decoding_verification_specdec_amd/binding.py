@@ -19,6 +19,7 @@ _LIB = None
 
 SPECDEC_F32 = 0
 SPECDEC_BF16 = 1
+SPECDEC_F16 = 2
 SPECDEC_MAX_K = 63
 
 
@@ -30,6 +31,21 @@ class _Options(ctypes.Structure):
     _fields_ = [("hot_event_begin", ctypes.c_void_p), ("hot_event_end", ctypes.c_void_p),
                 ("path", ctypes.c_int32), ("spin_limit", ctypes.c_int32),
                 ("draw_event_begin", ctypes.c_void_p), ("draw_event_end", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("position", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 # Execution paths of specdec_verify (include/specdec.h).
@@ -103,6 +119,23 @@ def load_library():
     lib.specdec_choose_k.restype = i32
     lib.specdec_plan_k.argtypes = [vp, i32, f64, i32, i32, i32, vp]
     lib.specdec_plan_k.restype = i32
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.specdec_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    lib.specdec_rope_frequencies.restype = i32
+    lib.specdec_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, vp, vp, vp,
+                                        vp, vp, vp]
+    lib.specdec_rope_append.restype = i32
+    lib.specdec_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.specdec_paged_attention_workspace_size.restype = sz
+    lib.specdec_paged_attention.argtypes = [vp, i64, i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, sz,
+                                            vp]
+    lib.specdec_paged_attention.restype = i32
+    lib.specdec_kv_weights.argtypes = [vp, i64, vp, i32, i32, i32, vp, vp, vp, f32, vp, vp]
+    lib.specdec_kv_weights.restype = i32
+    lib.specdec_kv_evict_workspace_size.argtypes = [i32, vp, i32]
+    lib.specdec_kv_evict_workspace_size.restype = sz
+    lib.specdec_kv_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
+    lib.specdec_kv_evict.restype = i32
     lib.specdec_status_string.argtypes = [i32]
     lib.specdec_status_string.restype = ctypes.c_char_p
     lib.specdec_version.argtypes = []
@@ -469,6 +502,265 @@ def specdec_plan_k(counters_host, c: float, k_min: int, k_max: int, k_default: i
                                            int(k_max), int(k_default), out.ctypes.data)
     _raise(status, "specdec_plan_k")
     return out
+
+
+SPECDEC_MAX_HEAD_DIM = 256
+_KV_DTYPES = {torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "turns": 3}
+
+
+class PagedKvCache:
+    """A paged key-value cache as the entry points of include/specdec.h take it: the pools ``k`` and
+    ``v`` [num_pages, page_size, kv_heads, head_dim] (bf16, fp16 or fp32; any strides with dense
+    rows, the same for both, so a head-major pool is passed as ``pool.transpose(1, 2)``),
+    ``page_table`` [B, max_pages] int32, and for caches that evict the slots' records ``weight``
+    (fp32) and ``position`` (int32) [num_pages, kv_heads, page_size].  Holds the tensors; checked
+    once here, so that a decode loop's calls pass it on as it is."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, *,
+                 weight: torch.Tensor | None = None, position: torch.Tensor | None = None):
+        if k.dim() != 4:
+            raise SpecdecError("k must be [num_pages, page_size, kv_heads, head_dim]")
+        if k.dtype not in _KV_DTYPES:
+            raise SpecdecError(f"k dtype {k.dtype} is not bf16/fp16/fp32")
+        if v.device != k.device or v.dtype != k.dtype or v.shape != k.shape:
+            raise SpecdecError("v must have the device, dtype and shape of k")
+        pages, page_size, heads, dim = (int(x) for x in k.shape)
+        used = [n for n, size in enumerate(k.shape) if size > 1]
+        if any(k.stride(n) != v.stride(n) for n in used):
+            raise SpecdecError("v must have the strides of k")
+        if dim > 1 and k.stride(3) != 1:
+            raise SpecdecError("the rows (last dimension) of k and v must be contiguous")
+        if page_table.dim() != 2:
+            raise SpecdecError("page_table must be [B, max_pages]")
+        self.B, max_pages = (int(x) for x in page_table.shape)
+        _check(page_table, "page_table", torch.int32, (self.B, max_pages), k.device)
+        _check(weight, "weight", torch.float32, (pages, heads, page_size), k.device, optional=True)
+        _check(position, "position", torch.int32, (pages, heads, page_size), k.device, optional=True)
+        self.k, self.v, self.page_table, self.weight, self.position = (k, v, page_table, weight,
+                                                                       position)
+        self.device, self.dtype = k.device, k.dtype
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
+        self.max_pages = max_pages
+        self._c = _KvCache(_ptr(k), _ptr(v), _KV_DTYPES[k.dtype], pages, page_size, heads, dim,
+                           max_pages, k.stride(0), k.stride(1), k.stride(2), _ptr(page_table),
+                           _ptr(weight), _ptr(position))
+        self._ref = ctypes.addressof(self._c)
+
+
+def _call(cache: PagedKvCache, stream, fn, name: str, *args):
+    """fn(*args, stream) with the cache's device current (a launch goes to the current device)."""
+    dev = cache.device
+    if dev.type != "cuda":
+        raise SpecdecError(f"the cache is on {dev}, expected a GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise SpecdecError(f"stream is on {stream.device}, expected {dev}")
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        _raise(status, name)
+
+
+def _tokens(t: torch.Tensor, name: str, cache: PagedKvCache, B: int, T: int, heads: int) -> int:
+    """Checks a [B, T, heads, head_dim] tensor of the cache's type with dense tokens evenly spaced;
+    returns the spacing in elements."""
+    if t.device != cache.device:
+        raise SpecdecError(f"{name} is on {t.device}, expected {cache.device}")
+    if t.dtype != cache.dtype:
+        raise SpecdecError(f"{name} has dtype {t.dtype}, expected {cache.dtype}")
+    if t.shape != (B, T, heads, cache.head_dim):
+        raise SpecdecError(f"{name} has shape {tuple(t.shape)}, expected "
+                           f"{(B, T, heads, cache.head_dim)}")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (heads > 1 and s2 != cache.head_dim):
+        raise SpecdecError(f"the heads and rows of {name} must be contiguous")
+    if B > 1 and T > 1 and s0 != T * s1:
+        raise SpecdecError(f"the tokens of {name} must be evenly spaced")
+    return s1 if T > 1 else s0
+
+
+def _round_shape(q: torch.Tensor, cache: PagedKvCache):
+    if q.dim() != 4:
+        raise SpecdecError("q must be [B, K+1, heads, head_dim]")
+    B, T, heads, _ = q.shape
+    if B != cache.B:
+        raise SpecdecError(f"q has {B} sequences, the cache's page table {cache.B}")
+    if T < 1:
+        raise SpecdecError("q must hold K+1 >= 1 tokens a sequence")
+    return B, T, heads
+
+
+def _scale_of(scale, cache: PagedKvCache) -> float:
+    return cache.head_dim ** -0.5 if scale is None else float(scale)
+
+
+def specdec_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "plain",
+                             factor: float = 1.0, original_len: float = 0.0,
+                             turns_low: float = 1.0, turns_high: float = 32.0) -> np.ndarray:
+    """Angular frequencies of the rotary pairs (host float64 [rotary_dim / 2]); ``scaling``: "plain",
+    "linear" (positions divided by ``factor``), "base" (a larger base) or "turns" (by each pair's
+    number of turns over ``original_len``).  Copy them to the device for specdec_rope_append."""
+    if scaling not in _ROPE_SCALINGS:
+        raise SpecdecError(f"scaling {scaling!r} is not one of {sorted(_ROPE_SCALINGS)}")
+    out = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.float64)
+    status = load_library().specdec_rope_frequencies(
+        int(rotary_dim), float(base), _ROPE_SCALINGS[scaling], float(factor), float(original_len),
+        float(turns_low), float(turns_high), out.ctypes.data)
+    _raise(status, "specdec_rope_frequencies")
+    return out
+
+
+def specdec_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKvCache,
+                        kv_len: torch.Tensor, inv_freq: torch.Tensor | None, *,
+                        interleaved: bool = False, rope_scale: float = 1.0,
+                        num_draft: torch.Tensor | None = None,
+                        first_pos: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Rotate a round's new tokens and append them to the cache.  q [B, K+1, heads, head_dim], k and v
+    [B, K+1, kv_heads, head_dim] in the cache's type (slices of a fused projection included), kv_len
+    [B] int32 slots in use, inv_freq [rotary_dim / 2] float64 on the device (None: nothing is
+    rotated), num_draft / first_pos [B] int32 or None (K; kv_len).  Returns the rotated q (``out``,
+    which may be q itself), enqueued on ``stream`` without synchronising."""
+    lib = load_library()
+    B, T, heads = _round_shape(q, cache)
+    dev = cache.device
+    qs = _tokens(q, "q", cache, B, T, heads)
+    ks = _tokens(k, "k", cache, B, T, cache.kv_heads)
+    vs = _tokens(v, "v", cache, B, T, cache.kv_heads)
+    _check(kv_len, "kv_len", torch.int32, (B,), dev)
+    _check(num_draft, "num_draft", torch.int32, (B,), dev, optional=True)
+    _check(first_pos, "first_pos", torch.int32, (B,), dev, optional=True)
+    half = 0
+    if inv_freq is not None:
+        half = int(inv_freq.numel())
+        _check(inv_freq, "inv_freq", torch.float64, (half,), dev)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((B, T, heads, cache.head_dim), dtype=cache.dtype, device=dev)
+    else:
+        _check(out, "out", cache.dtype, (B, T, heads, cache.head_dim), dev)
+    rope = _Rope(_ptr(inv_freq), 2 * half, 1 if interleaved else 0, rope_scale)
+    _call(cache, stream, lib.specdec_rope_append, "specdec_rope_append", q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), qs, ks, vs, B, T - 1, heads, _ptr(num_draft), kv_len.data_ptr(),
+          _ptr(first_pos), ctypes.addressof(rope), cache._ref, out.data_ptr())
+    return out
+
+
+def specdec_paged_attention_workspace_size(B: int, K: int, heads: int, kv_heads: int,
+                                           head_dim: int) -> int:
+    return int(load_library().specdec_paged_attention_workspace_size(
+        int(B), int(K), int(heads), int(kv_heads), int(head_dim)))
+
+
+def new_paged_attention_workspace(cache: PagedKvCache, K: int, heads: int, stream=None) -> torch.Tensor:
+    """A workspace for specdec_paged_attention calls of up to K drafts (uninitialised: the library
+    needs none), allocated for ``stream``."""
+    need = specdec_paged_attention_workspace_size(cache.B, K, heads, cache.kv_heads, cache.head_dim)
+    with _on(stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+
+
+def specdec_paged_attention(q: torch.Tensor, cache: PagedKvCache, kv_len: torch.Tensor, *,
+                            num_draft: torch.Tensor | None = None, scale: float | None = None,
+                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                            want_lse: bool = False, workspace: torch.Tensor | None = None,
+                            stream=None):
+    """Attention of a round's tokens (already appended) over the cache.  q [B, K+1, heads, head_dim],
+    kv_len [B] int32 slots before the round, num_draft [B] int32 or None, scale (default
+    head_dim^-0.5).  Returns (out [B, K+1, heads, head_dim], lse [B, K+1, heads] fp32 or None; lse
+    when ``want_lse`` or a tensor for it is given), enqueued on ``stream`` without synchronising.
+    ``workspace``: new_paged_attention_workspace, reusable across calls; None allocates one."""
+    lib = load_library()
+    B, T, heads = _round_shape(q, cache)
+    dev = cache.device
+    qs = _tokens(q, "q", cache, B, T, heads)
+    _check(kv_len, "kv_len", torch.int32, (B,), dev)
+    _check(num_draft, "num_draft", torch.int32, (B,), dev, optional=True)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((B, T, heads, cache.head_dim), dtype=cache.dtype, device=dev)
+    else:
+        _check(out, "out", cache.dtype, (B, T, heads, cache.head_dim), dev)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (B, T, heads), dev)
+    elif want_lse:
+        with _on(stream):
+            lse = torch.empty((B, T, heads), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = new_paged_attention_workspace(cache, T - 1, heads, stream)
+    else:
+        _check_workspace(workspace, dev)
+    _call(cache, stream, lib.specdec_paged_attention, "specdec_paged_attention", q.data_ptr(), qs, B,
+          T - 1, heads, _ptr(num_draft), kv_len.data_ptr(), _scale_of(scale, cache), cache._ref,
+          out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return out, lse
+
+
+def _check_workspace(workspace: torch.Tensor, dev):
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise SpecdecError(f"workspace must be a contiguous uint8 tensor on {dev}")
+
+
+def specdec_kv_weights(q: torch.Tensor, lse: torch.Tensor, cache: PagedKvCache,
+                       kv_len: torch.Tensor, *, num_draft: torch.Tensor | None = None,
+                       accept_len: torch.Tensor | None = None, scale: float | None = None,
+                       stream=None) -> torch.Tensor:
+    """Add to ``cache.weight`` (in place; returned) the attention weights that the accepted rows of a
+    round gave each slot: q, lse, kv_len, num_draft and scale of the attention call, accept_len [B]
+    int32 of the verify step (None: every row)."""
+    lib = load_library()
+    B, T, heads = _round_shape(q, cache)
+    dev = cache.device
+    if cache.weight is None:
+        raise SpecdecError("the cache has no weight records")
+    qs = _tokens(q, "q", cache, B, T, heads)
+    _check(lse, "lse", torch.float32, (B, T, heads), dev)
+    _check(kv_len, "kv_len", torch.int32, (B,), dev)
+    _check(num_draft, "num_draft", torch.int32, (B,), dev, optional=True)
+    _check(accept_len, "accept_len", torch.int32, (B,), dev, optional=True)
+    _call(cache, stream, lib.specdec_kv_weights, "specdec_kv_weights", q.data_ptr(), qs,
+          lse.data_ptr(), B, T - 1, heads, _ptr(num_draft), _ptr(accept_len), kv_len.data_ptr(),
+          _scale_of(scale, cache), cache._ref)
+    return cache.weight
+
+
+def new_kv_evict_workspace(cache: PagedKvCache, budget: int, stream=None) -> torch.Tensor:
+    """A workspace for specdec_kv_evict calls with this budget (uninitialised), allocated for
+    ``stream``."""
+    need = int(load_library().specdec_kv_evict_workspace_size(cache.B, cache._ref, int(budget)))
+    with _on(stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+
+
+def specdec_kv_evict(cache: PagedKvCache, kv_len: torch.Tensor, budget: int, *, keep_first: int = 0,
+                     keep_last: int = 0, new_len: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Evict the lightest slots of every sequence longer than ``budget``, in place in the cache's k,
+    v, weight and position.  Returns new_len [B] int32 (``new_len`` may be kv_len itself; None
+    allocates it): min(kv_len, budget), or -1 for an invalid sequence."""
+    lib = load_library()
+    dev = cache.device
+    if cache.weight is None or cache.position is None:
+        raise SpecdecError("the cache has no weight and position records")
+    _check(kv_len, "kv_len", torch.int32, (cache.B,), dev)
+    if new_len is None:
+        with _on(stream):
+            new_len = torch.empty(cache.B, dtype=torch.int32, device=dev)
+    else:
+        _check(new_len, "new_len", torch.int32, (cache.B,), dev)
+    if workspace is None:
+        workspace = new_kv_evict_workspace(cache, budget, stream)
+    else:
+        _check_workspace(workspace, dev)
+    _call(cache, stream, lib.specdec_kv_evict, "specdec_kv_evict", cache._ref, kv_len.data_ptr(),
+          cache.B, int(budget), int(keep_first), int(keep_last), new_len.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return new_len
 
 
 def inputs_to_device(inp, device) -> dict:

@@ -13,8 +13,10 @@ PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / "kernels.hip", PKG / "csrc" / "fused.hip", PKG / "csrc" / "small.hip", PKG / "csrc" / "ngram.hip",
            PKG / "csrc" / "commit.hip", PKG / "csrc" / "noalloc.hip", PKG / "csrc" / "quad.hip",
-           PKG / "csrc" / "telemetry.hip", PKG / "csrc" / "api.cpp", PKG / "csrc" / "telemetry.cpp"]
-HEADERS = [PKG / "csrc" / "kernels.h", PKG / "csrc" / "verify_dev.h", PKG / "csrc" / "wave_ops.h", ROOT / "include" / "specdec.h"]
+           PKG / "csrc" / "telemetry.hip", PKG / "csrc" / "rope.hip", PKG / "csrc" / "paged_attention.hip",
+           PKG / "csrc" / "kv_weights.hip", PKG / "csrc" / "kv_evict.hip",
+           PKG / "csrc" / "api.cpp", PKG / "csrc" / "telemetry.cpp", PKG / "csrc" / "paged_api.cpp"]
+HEADERS = [PKG / "csrc" / "kernels.h", PKG / "csrc" / "paged.h", PKG / "csrc" / "verify_dev.h", PKG / "csrc" / "wave_ops.h", ROOT / "include" / "specdec.h"]
 OUTPUT = PKG / "libspecdec.so"
 ARCH = os.environ.get("SPECDEC_OFFLOAD_ARCH", "gfx950")
 
