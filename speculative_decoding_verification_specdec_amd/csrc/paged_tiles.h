@@ -1,0 +1,118 @@
+// Matrix tiles over the paged cache, shared by the attention and the weights kernels.
+//
+// A wave takes kKeys slots of one kv head and 16-row groups of query rows.  Scores come transposed,
+//   S^T [slots x rows] = K [slots x dim] . Q^T [dim x rows],
+// so that a lane's four results belong to one row (its column lane % 16) and to the slots
+// 4 (lane / 16) + r: statistics of a row stay in a lane and its three partners 16 lanes apart, and the
+// results are already where the second product wants them,
+//   O^T [dim x rows] = V^T [dim x slots] . P^T [slots x rows],
+// whose operand takes the slots of a lane's group in any order that both sides share.
+//
+// Operands go straight from memory into registers, each byte of the cache once: an instruction's 64
+// lanes read 16 keys x 64 bytes (K) or 4 whole rows of V.  V's operand needs one dim of eight slots in a
+// lane while a lane has loaded eight dims of each of its eight slots: the 8 x 8 block is turned within
+// the lane by byte permutes, 32 of them a tile, so neither LDS nor a shuffle lies on the way.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "paged.h"
+
+namespace specdec {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+template <typename T>
+struct Half8;
+template <>
+struct Half8<__bf16> {
+  typedef __bf16 type __attribute__((ext_vector_type(8)));
+  typedef __bf16 pair __attribute__((ext_vector_type(2)));
+};
+template <>
+struct Half8<_Float16> {
+  typedef _Float16 type __attribute__((ext_vector_type(8)));
+  typedef _Float16 pair __attribute__((ext_vector_type(2)));
+};
+
+__device__ __forceinline__ f32x4 mma16(const u32x4& a, const u32x4& b, const f32x4& c, __bf16) {
+  typedef Half8<__bf16>::type H;
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(H, a), __builtin_bit_cast(H, b),
+                                                 c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma16(const u32x4& a, const u32x4& b, const f32x4& c, _Float16) {
+  typedef Half8<_Float16>::type H;
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(H, a), __builtin_bit_cast(H, b),
+                                                c, 0, 0, 0);
+}
+// Four products of depth 4: element e of the lanes' vectors together.
+__device__ __forceinline__ f32x4 mma16(const u32x4& a, const u32x4& b, f32x4 c, float) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  typedef typename Half8<T>::pair P;
+  P p = {static_cast<T>(lo), static_cast<T>(hi)};
+  return __builtin_bit_cast(unsigned, p);
+}
+
+// kDim: head_dim rounded up to 64, 128 or 256; kFull: equal to it; else the rest of a
+// row is taken as 0.
+template <typename T, int kDim, bool kFull>
+struct Tile {
+  static constexpr int kHalf = sizeof(T) == 2;         // a 16-bit type
+  static constexpr int kKeys = kHalf ? 32 : 16;        // slots a tile
+  static constexpr int kSub = kKeys / 16;              // 16-slot groups of the scores
+  static constexpr int kVec = 16 / sizeof(T);          // elements of 16 bytes
+  static constexpr int kSteps = kDim / (4 * kVec);     // 16-byte loads of a lane for one row of K or Q
+  static constexpr int kChunk = kDim / 16;             // elements a lane takes of a row of V
+  static constexpr int kOut = kDim / 16;               // 16-dim groups of the output
+  static constexpr int kRowsV = kKeys / 4;             // rows of V a lane takes
+  static constexpr int kWords = kChunk * sizeof(T) / 4;
+
+  // A lane's part of a row of K or Q: kVec elements from 4 kVec s + kVec g on, for every step s.  The row
+  // lies `off` elements from `base`; a wave-uniform base keeps the 64-bit part of the address scalar.
+  static __device__ __forceinline__ void load_row(u32x4 (&f)[kSteps], const T* base, unsigned off, int g,
+                                                  int dim) {
+    const unsigned at = (off + kVec * g) * static_cast<unsigned>(sizeof(T));
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      f[s] = u32x4{0, 0, 0, 0};
+      if (kFull || 4 * kVec * s + kVec * g < dim)
+        f[s] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base) + at + 64 * s);
+    }
+  }
+
+  // kChunk elements of a row of V from kChunk * (lane % 16) on.
+  static __device__ __forceinline__ void load_v(unsigned (&f)[kWords], const T* base, unsigned off, int col,
+                                                int dim) {
+    const unsigned at = (off + kChunk * col) * static_cast<unsigned>(sizeof(T));
+    const char* p = reinterpret_cast<const char*>(base);
+    if constexpr (kWords == 2) {
+      u32x2 x = {0, 0};
+      if (kFull || kChunk * col < dim) x = *reinterpret_cast<const u32x2*>(p + at);
+      f[0] = x[0];
+      f[1] = x[1];
+    } else {
+#pragma unroll
+      for (int w = 0; w < kWords; w += 4) {
+        u32x4 x = {0, 0, 0, 0};
+        if (kFull || kChunk * col + w * 4 / static_cast<int>(sizeof(T)) < dim)
+          x = *reinterpret_cast<const u32x4*>(p + at + 4 * w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[w + e] = x[e];
+      }
+    }
+  }
+
+  // Slot within the tile of a lane's score r of group sub, and of its V row 4 sub + r.
+  static __device__ __forceinline__ int slot_of(int sub, int r, int g) { return 16 * sub + 4 * g + r; }
+};
+
+}  // namespace specdec

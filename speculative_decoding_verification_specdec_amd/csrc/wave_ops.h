@@ -11,6 +11,7 @@
 namespace specdec {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kTempMin = 1e-6f;  // smallest non-zero temperature (SPECDEC_TEMPERATURE_MIN)
 
 // A temperature is 0 (greedy) or a finite value of at least kTempMin.
