@@ -15,6 +15,11 @@ constexpr int kUnit = 128;          // slots of one unit of work
 constexpr int kQueryRegs = 16;      // registers that a wave's query operands may take
 constexpr int kAttendGroups = 512;  // workgroups at most (two a CU)
 
+// A segment that lies in several ranges: parts of workgroups w .. w + parts - 1 (parts 0: none).
+struct alignas(16) CutSegment {
+  int parts, b, seg, first_slot;
+};
+
 // How a call is cut.  A segment is one (sequence, kv head, chunk of query rows); its units, and those of
 // all segments one after the other, are dealt out evenly to `groups` workgroups in contiguous ranges.
 struct AttendPlan {
@@ -26,7 +31,7 @@ struct AttendPlan {
   int dim;              // kDim of the kernel
   int page_shift;       // log2(page_size), or -1
   float scale_log2;     // scale * log2(e)
-  long long* prefix;    // [B + 1] units before each sequence, per (kv head, chunk)
+  CutSegment* cut;      // [groups] the segment that a workgroup's range ends in the first part of
   float* part_o;        // [2 groups][rows][dim] unnormalised outputs of cut segments
   float* part_m;        // [2 groups][rows] their maxima (of scores * log2(e))
   float* part_l;        // [2 groups][rows] their sums
@@ -150,10 +155,10 @@ struct AttendWave {
 #pragma unroll
     for (int sub = 0; sub < L::kSub; ++sub) {
       if constexpr (kFast)
-        L::load_row(kf[sub], kpool + r.at[sub],
+        L::template load_row<true>(kf[sub], kpool + r.at[sub],
                     static_cast<unsigned>(col) * static_cast<unsigned>(c.slot_stride), g, c.dim);
       else
-        L::load_row(kf[sub], kpool + shfl64(r.at[0], 16 * sub + col), 0u, g, c.dim);
+        L::template load_row<true>(kf[sub], kpool + shfl64(r.at[0], 16 * sub + col), 0u, g, c.dim);
     }
   }
 
@@ -161,11 +166,11 @@ struct AttendWave {
 #pragma unroll
     for (int x = 0; x < L::kRowsV; ++x) {
       if constexpr (kFast)
-        L::load_v(vf[x], vpool + r.at[x / 4],
+        L::template load_v<true>(vf[x], vpool + r.at[x / 4],
                   static_cast<unsigned>(4 * g + x % 4) * static_cast<unsigned>(c.slot_stride), col,
                   c.dim);
       else
-        L::load_v(vf[x], vpool + shfl64(r.at[0], L::slot_of(x / 4, x % 4, g)), 0u, col, c.dim);
+        L::template load_v<true>(vf[x], vpool + shfl64(r.at[0], L::slot_of(x / 4, x % 4, g)), 0u, col, c.dim);
     }
   }
 
@@ -360,6 +365,78 @@ struct AttendWave {
   }
 };
 
+// Four elements from d on of an output row, and with the first its lse; a row past the last token is 0.
+template <typename T>
+__device__ __forceinline__ void write_row(const AttendArgs& a, const KvArgs& c, long long row, bool used,
+                                          int d, f32x4 sum, float top, float total) {
+  const float inv = 1.f / total;
+  if (!used) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+  else sum *= inv;
+  T* out = static_cast<T*>(a.out) + row * c.dim + d;
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<u32x2*>(out) = u32x2{pack2<T>(sum[0], sum[1]), pack2<T>(sum[2], sum[3])};
+  else
+    *reinterpret_cast<f32x4*>(out) = sum;
+  if (d == 0 && a.lse)
+    a.lse[row] = !used ? -INFINITY : top == -INFINITY ? __builtin_nanf("") : top * kLn2 + logf(total);
+}
+
+// Adds up the parts of a cut segment: workgroup (w, y) the rows 16 y .. of the one whose first part
+// workgroup w of the split holds.  dim / 4 lanes share a row, so a wave loads 256 / dim parts' worth at once,
+// four of them ahead.
+template <typename T, int kDim>
+__global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs a, KvArgs c,
+                                                                     AttendPlan plan) {
+  constexpr int kLanes = kDim / 4;                    // lanes of a row
+  constexpr int kRowsOnce = kAttendThreads / kLanes;  // rows at once
+  const int w = blockIdx.x;
+  const CutSegment cut = plan.cut[w];
+  if (cut.parts == 0) return;
+  const RoundRows r = round_rows(c, a.num_draft, a.kv_len, cut.b, a.K);
+  const int group = a.q_heads / c.heads;
+  const int h = cut.seg / plan.chunks, chunk = cut.seg - h * plan.chunks;
+  const int d = threadIdx.x % kLanes * 4;
+  const int end = min(plan.rows, (a.K + 1) * group - chunk * plan.rows);
+  for (int local = blockIdx.y * kRowsOnce + threadIdx.x / kLanes; local < end; local += gridDim.y * kRowsOnce) {
+    const int qrow = chunk * plan.rows + local, i = qrow / group;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float top = -INFINITY, sum = 0.f;
+    if (i < r.n) {
+      constexpr int kAhead = 8;
+      for (int p = 0; p < cut.parts; p += kAhead) {
+        f32x4 x[kAhead];
+        float m[kAhead], l[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          const int q = min(p + e, cut.parts - 1);
+          const long long at = (2LL * (w + q) + (q == 0 ? cut.first_slot : 0)) * plan.rows + local;
+          x[e] = *reinterpret_cast<const f32x4*>(plan.part_o + at * kDim + d);
+          m[e] = plan.part_m[at];
+          l[e] = plan.part_l[at];
+        }
+        float now = top;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) now = fmaxf(now, m[e]);
+        const float base = now == -INFINITY ? 0.f : now;
+        const float old = exp2_hw(top - base);
+        o *= old;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (p + e >= cut.parts) break;
+          const float f = exp2_hw(m[e] - base);
+          o += x[e] * f;
+          sum += l[e] * f;
+        }
+        top = now;
+      }
+    }
+    if (d < c.dim)
+      write_row<T>(a, c, (static_cast<long long>(cut.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
+                   i < r.n, d, o, top, sum);
+  }
+}
+
 // kFast: head_dim is kDim, pages are whole groups of 16 slots and 16 slots lie within 2^32 bytes.
 template <typename T, int kDim, bool kFast, int kRowTiles, int kOccupancy>
 __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kernel(AttendArgs a, KvArgs c,
@@ -404,14 +481,20 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
   const int w = groups == plan.groups
                     ? static_cast<int>(blockIdx.x % 8 * (plan.groups / 8) + blockIdx.x / 8)
                     : static_cast<int>(blockIdx.x);
-  if (w == 0) {  // for the join
-    long long x = before;
-    for (int b = run0; b < run1; ++b) {
-      plan.prefix[b] = x;
-      x += units_of(round_rows(c, a.num_draft, a.kv_len, b, a.K));
-    }
-    if (tid == 0) plan.prefix[a.B] = all;
+  // Sequences without units are invalid: their rows are NaN.
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const RoundRows r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
+    if (r.n > 0) continue;
+    const long long row = static_cast<long long>(b) * (a.K + 1) * a.q_heads;
+    const long long bad = static_cast<long long>(r.rows) * a.q_heads;
+    const long long rows = (a.K + 1LL) * a.q_heads;
+    T* out = static_cast<T*>(a.out) + row * c.dim;
+    for (long long x = tid; x < rows * c.dim; x += kAttendThreads)
+      out[x] = from_float<T>(x < bad * c.dim ? __builtin_nanf("") : 0.f);
+    for (long long x = tid; a.lse && x < rows; x += kAttendThreads)
+      a.lse[row + x] = x < bad ? __builtin_nanf("") : -INFINITY;
   }
+  if (tid == 0) plan.cut[w].parts = 0;
   if (w >= groups) return;
   const long long begin = range_begin(w, total_units, groups);
   const long long end = range_begin(w + 1, total_units, groups);
@@ -472,7 +555,7 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
 #pragma unroll
       for (int x = 0; x < L::kSteps; ++x) qt[x] = u32x4{0, 0, 0, 0};
       if (i < n)
-        L::load_row(qt,
+        L::template load_row<false>(qt,
                     static_cast<const T*>(a.q) + (static_cast<long long>(b) * (a.K + 1) + i) * a.q_stride +
                         static_cast<long long>(h * group + qrow - i * group) * c.dim,
                     0u, g, c.dim);
@@ -484,7 +567,9 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
           s.q[t][x] = qt[x];
       }
     }
-    s.walk(at * kTilesUnit + kw, min(stop * kTilesUnit, (len + n + L::kKeys - 1) / L::kKeys), key_waves);
+    if (row0 < n * group)  // (a wave without rows has nothing to read)
+      s.walk(at * kTilesUnit + kw, min(stop * kTilesUnit, (len + n + L::kKeys - 1) / L::kKeys),
+             key_waves);
 
     // Join the waves that split the slots, 16 rows a round, and write the segment's rows or, if another
     // workgroup holds the rest of it, this piece's part.
@@ -535,20 +620,10 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
         const float rtop = sh_top[rwi][16 * t + rr], rsum = sh_sum[rwi][16 * t + rr];
         if (whole) {
           const int qrow = chunk * plan.rows + local, i = qrow / group;
-          if (i < n && d < c.dim) {
-            const long long out_row =
-                (static_cast<long long>(b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group;
-            const float inv = 1.f / rsum;
-            T* out = static_cast<T*>(a.out) + out_row * c.dim + d;
-            if constexpr (L::kHalf)
-              *reinterpret_cast<u32x2*>(out) =
-                  u32x2{pack2<T>(sum[0] * inv, sum[1] * inv), pack2<T>(sum[2] * inv, sum[3] * inv)};
-            else
-              *reinterpret_cast<f32x4*>(out) = sum * inv;
-            if (d == 0 && a.lse)
-              a.lse[out_row] = rtop == -INFINITY ? __builtin_nanf("") : rtop * kLn2 + logf(rsum);
-          }
-        } else {
+          if (i <= a.K && d < c.dim)
+            write_row<T>(a, c, (static_cast<long long>(b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
+                         i < n, d, sum, rtop, rsum);
+        } else if (chunk * plan.rows + local < n * group) {
           const long long at_row = part * plan.rows + local;
           *reinterpret_cast<f32x4*>(plan.part_o + at_row * kDim + d) = sum;
           if (d == 0) {
@@ -558,6 +633,10 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
         }
       }
       __syncthreads();
+    }
+    if (at == 0 && stop < units && tid == 0) {
+      const int last = owner_of(begin + (end - begin - left) + units - 1, total_units, groups);
+      plan.cut[w] = CutSegment{last - w + 1, b, seg, slot_of_part};
     }
     slot_of_part = 1;
     left -= stop - at;
@@ -572,6 +651,14 @@ __global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kerne
   }
 }
 
+template <typename T, int kDim>
+void launch_join(const AttendArgs& a, const KvArgs& c, const AttendPlan& p) {
+  constexpr int kRowsOnce = kAttendThreads / (kDim / 4);
+  const int rows = p.rows < (a.K + 1) * (a.q_heads / c.heads) ? p.rows : (a.K + 1) * (a.q_heads / c.heads);
+  const dim3 grid(p.groups, (rows + kRowsOnce - 1) / kRowsOnce);
+  attend_join_kernel<T, kDim><<<grid, kAttendThreads, 0, a.stream>>>(a, c, p);
+}
+
 template <typename T, int kDim, bool kFast>
 void launch_attend_dim(const AttendArgs& a, const KvArgs& c, const AttendPlan& p) {
   const dim3 grid(p.groups), block(kAttendThreads);
@@ -583,6 +670,7 @@ void launch_attend_dim(const AttendArgs& a, const KvArgs& c, const AttendPlan& p
     else if constexpr (kDim == 64 || sizeof(T) == 2)
       attend_split_kernel<T, kDim, kFast, 4, 1><<<grid, block, 0, a.stream>>>(a, c, p);
   }
+  launch_join<T, kDim>(a, c, p);
 }
 
 template <typename T>

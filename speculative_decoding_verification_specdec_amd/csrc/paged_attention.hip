@@ -9,91 +9,14 @@
 // bytes.  Sequences differ in length and one long one must not decide the time: the units of 128 slots of
 // all (sequence, kv head, row chunk) segments are laid end to end and cut into equal contiguous ranges,
 // one a workgroup.  A segment that lies in one range is written at once; the others leave one part a
-// range (at most two a workgroup), which the join adds up.
+// range (at most two a workgroup), which the join adds up.  A range ends in the first part of at most one
+// cut segment, which it notes, so the join has as many workgroups to look at as there are ranges.
 #include <hip/hip_runtime.h>
 
 #include "attend_dev.h"
 
 namespace specdec {
 namespace {
-
-// One wave per output row: rows past the last new token are 0, those of an invalid sequence NaN, those
-// of a cut segment the sum of its parts; the others are there already.
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, KvArgs c, AttendPlan plan,
-                                                          int dtype) {
-  const int lane = threadIdx.x & 63;
-  const long long rows = static_cast<long long>(a.B) * (a.K + 1) * a.q_heads;
-  const int group = a.q_heads / c.heads;
-  const long long all = plan.prefix[a.B] * c.heads * plan.chunks;
-  const int groups = active_groups(all, plan.groups);
-  for (long long row = blockIdx.x * 4LL + (threadIdx.x >> 6); row < rows; row += gridDim.x * 4LL) {
-    const long long token = row / a.q_heads;
-    const int h = static_cast<int>(row - token * a.q_heads);
-    const int b = static_cast<int>(token / (a.K + 1));
-    const int i = static_cast<int>(token - static_cast<long long>(b) * (a.K + 1));
-    const RoundRows r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
-    float o[kMaxHeadDim / 64] = {};
-    float lse = -INFINITY;
-    if (i < r.rows) {
-      if (r.n > 0) {
-        const int kvh = h / group;
-        const int qrow = i * group + h - kvh * group, chunk = qrow / plan.rows;
-        const int local = qrow - chunk * plan.rows;
-        const long long units = units_of(r);
-        const long long u0 = plan.prefix[b] * c.heads * plan.chunks + (kvh * plan.chunks + chunk) * units;
-        const int w0 = owner_of(u0, all, groups), w1 = owner_of(u0 + units - 1, all, groups);
-        if (w0 == w1) continue;
-        // The first range holds its piece last unless the segment starts with it; the others start with it.
-        const int slot0 = range_begin(w0, all, groups) == u0 ? 0 : 1;
-        float top = -INFINITY, sum = 0.f;
-        for (int w = w0; w <= w1; w += 64) {
-          const int n = min(64, w1 - w + 1);
-          float m = -INFINITY, l = 0.f;
-          if (lane < n) {
-            const long long at = (2LL * (w + lane) + (w + lane == w0 ? slot0 : 0)) * plan.rows + local;
-            m = plan.part_m[at];
-            l = plan.part_l[at];
-          }
-          const float now = fmaxf(top, wave_max_f(m)), base = now == -INFINITY ? 0.f : now;
-          const float old = exp2_hw(top - base), f = exp2_hw(m - base);
-          sum = sum * old + wave_sum_f(l * f);
-#pragma unroll
-          for (int e = 0; e < kMaxHeadDim / 64; ++e) o[e] *= old;
-          for (int x = 0; x < n; ++x) {
-            const float fx = __shfl(f, x, 64);
-            const float* src =
-                plan.part_o +
-                ((2LL * (w + x) + (w + x == w0 ? slot0 : 0)) * plan.rows + local) * plan.dim;
-#pragma unroll
-            for (int e = 0; e < kMaxHeadDim / 64; ++e)
-              if (lane + 64 * e < c.dim) o[e] += fx * src[lane + 64 * e];
-          }
-          top = now;
-        }
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int e = 0; e < kMaxHeadDim / 64; ++e) o[e] *= inv;
-        lse = top == -INFINITY ? __builtin_nanf("") : top * kLn2 + logf(sum);
-      } else {
-        lse = __builtin_nanf("");
-#pragma unroll
-        for (int e = 0; e < kMaxHeadDim / 64; ++e) o[e] = lse;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kMaxHeadDim / 64; ++e) {
-      const int d = lane + 64 * e;
-      if (d >= c.dim) continue;
-      if (dtype == 0)
-        static_cast<float*>(a.out)[row * c.dim + d] = o[e];
-      else if (dtype == 1)
-        static_cast<__bf16*>(a.out)[row * c.dim + d] = from_float<__bf16>(o[e]);
-      else
-        static_cast<_Float16*>(a.out)[row * c.dim + d] = from_float<_Float16>(o[e]);
-    }
-    if (lane == 0 && a.lse) a.lse[row] = lse;
-  }
-}
 
 // The row tiles and waves for the rows of a group: 16-row tiles a wave as needed up to what the
 // registers hold (4; 1 for the widest heads), then more waves by rows, then chunks.
@@ -117,15 +40,15 @@ size_t align16(size_t x) { return (x + 15) & ~size_t{15}; }
 size_t attend_workspace_bytes(int B, int K, int q_heads, int kv_heads, int dim) {
   const AttendPlan p = make_plan(B, K, q_heads, kv_heads, dim, false);  // (f32 has no more rows)
   const size_t part_rows = 2 * static_cast<size_t>(p.groups) * p.rows;
-  return align16((static_cast<size_t>(B) + 1) * 8) + part_rows * p.dim * 4 + 2 * align16(part_rows * 4);
+  return p.groups * sizeof(CutSegment) + part_rows * p.dim * 4 + 2 * align16(part_rows * 4);
 }
 
 hipError_t launch_attend(const AttendArgs& a, const KvArgs& c, int dtype) {
   AttendPlan p = make_plan(a.B, a.K, a.q_heads, c.heads, c.dim, dtype == 0);
   const size_t part_rows = 2 * static_cast<size_t>(p.groups) * p.rows;
   char* ws = static_cast<char*>(a.workspace);
-  p.prefix = reinterpret_cast<long long*>(ws);
-  ws += align16((static_cast<size_t>(a.B) + 1) * 8);
+  p.cut = reinterpret_cast<CutSegment*>(ws);
+  ws += p.groups * sizeof(CutSegment);
   p.part_o = reinterpret_cast<float*>(ws);
   ws += part_rows * p.dim * 4;
   p.part_m = reinterpret_cast<float*>(ws);
@@ -140,12 +63,6 @@ hipError_t launch_attend(const AttendArgs& a, const KvArgs& c, int dtype) {
     launch_attend_bf16(a, c, p);
   else
     launch_attend_f16(a, c, p);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  const long long rows = static_cast<long long>(a.B) * (a.K + 1) * a.q_heads;
-  const long long blocks = (rows + 3) / 4;
-  attend_join_kernel<<<static_cast<unsigned>(blocks < (1 << 20) ? blocks : 1 << 20), 256, 0, a.stream>>>(
-      a, c, p, dtype);
   return hipGetLastError();
 }
 
