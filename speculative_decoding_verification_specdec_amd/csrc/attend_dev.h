@@ -9,62 +9,81 @@
 
 namespace specdec {
 
-constexpr int kAttendWaves = 4;
-constexpr int kAttendThreads = 64 * kAttendWaves;
-constexpr int kUnit = 128;          // slots of one unit of work
-constexpr int kQueryRegs = 16;      // registers that a wave's query operands may take
-constexpr int kAttendGroups = 512;  // workgroups at most (two a CU)
+constexpr int kJoinThreads = 256;
 
-// A segment that lies in several ranges: parts of workgroups w .. w + parts - 1 (parts 0: none).
-struct alignas(16) CutSegment {
-  int parts, b, seg, first_slot;
+// A segment that lies in the ranges of several workgroups: parts of workgroups w .. w + parts - 1 (parts 0:
+// none); n: its sequence's new tokens.
+struct alignas(32) CutSegment {
+  int parts, b, seg, n;
 };
 
-// How a call is cut.  A segment is one (sequence, kv head, chunk of query rows); its units, and those of
-// all segments one after the other, are dealt out evenly to `groups` workgroups in contiguous ranges.
+// How a call is cut.  A segment is one (sequence, kv head, chunk of its query rows); its tiles, and those of all
+// segments one after the other, are dealt out evenly to 1 << log_ranges waves in contiguous ranges.
 struct AttendPlan {
-  int groups;
-  int row_waves;        // waves of a workgroup that hold different rows; the others split the slots
-  int chunks;           // row chunks of a (sequence, kv head)
-  int rows;             // rows of a chunk: 16 * row groups a wave * row_waves
-  int tile_rows;        // 16-row groups a wave
+  int log_ranges;
+  int log_waves;        // log2(ranges a workgroup), neighbouring ones
+  int wide;             // the kernel for many rows: one range a workgroup
+  int rows;             // rows of a chunk: 16 a row tile
   int dim;              // kDim of the kernel
   int page_shift;       // log2(page_size), or -1
   float scale_log2;     // scale * log2(e)
-  CutSegment* cut;      // [groups] the segment that a workgroup's range ends in the first part of
-  float* part_o;        // [2 groups][rows][dim] unnormalised outputs of cut segments
-  float* part_m;        // [2 groups][rows] their maxima (of scores * log2(e))
-  float* part_l;        // [2 groups][rows] their sums
+  CutSegment* cut;      // [workgroups] the cut segment whose first part a workgroup holds
+  float* part_o;        // [2 workgroups][rows][dim] unnormalised outputs: of the segment that comes from the
+  float* part_m;        // [2 workgroups][rows]      workgroup before (0) and of the one that begins here (1);
+  float* part_l;        // [2 workgroups][rows]      their bases (of scores * log2(e)) and sums
 };
 
-__device__ __forceinline__ long long units_of(const RoundRows& r) {
-  return r.n > 0 ? (static_cast<long long>(r.len) + r.n + kUnit - 1) / kUnit : 0;
+// Row chunks of a sequence with n new tokens; tiles of its slots; tiles of all its segments (none if it
+// is invalid).
+__device__ __forceinline__ int chunks_of(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
+template <int kKeys>
+__device__ __forceinline__ int tiles_of(int len, int n) {
+  return (len + n - 1) / kKeys + 1;
 }
-// Workgroups that get a range: with fewer units than workgroups, one unit each.
-__device__ __forceinline__ int active_groups(long long total, int groups) {
-  return total < groups ? static_cast<int>(total) : groups;
+template <int kKeys>
+__device__ __forceinline__ long long work_of(const RoundRows& r, int heads, int group, int rows) {
+  return r.n > 0 ? static_cast<long long>(tiles_of<kKeys>(r.len, r.n)) * (heads * chunks_of(r.n, group, rows)) : 0;
 }
-// First unit of workgroup w, and the workgroup that holds a unit.
-__device__ __forceinline__ long long range_begin(long long w, long long total, int groups) {
-  return w * total / groups;
+// First tile of range w, and the range that holds a tile.  Fewer tiles than ranges: one tile each.
+__device__ __forceinline__ long long range_begin(long long w, long long total, int log_ranges) {
+  return total >> log_ranges == 0 ? min(w, total) : w * total >> log_ranges;
 }
-__device__ __forceinline__ int owner_of(long long unit, long long total, int groups) {
-  return static_cast<int>(((unit + 1) * groups - 1) / total);
+__device__ __forceinline__ int range_of(long long tile, long long total, int log_ranges) {
+  if (total >> log_ranges == 0) return static_cast<int>(tile);
+  // The w with w total <= (tile + 1) 2^log - 1 < (w + 1) total, by a quotient in f64 (both under 2^53)
+  // and a correction by one.
+  const long long n = ((tile + 1) << log_ranges) - 1;
+  long long q = static_cast<long long>(static_cast<double>(n) / static_cast<double>(total));
+  if (q * total > n) --q;
+  if ((q + 1) * total <= n) ++q;
+  return static_cast<int>(q);
 }
 
-// Maximum and sum over the four lanes 16 apart that share a row.
+// Maximum and sum over the four lanes 16 apart that share a row: each step swaps halves of two copies.
 __device__ __forceinline__ float row_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16, 64));
-  return fmaxf(x, __shfl_xor(x, 32, 64));
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned v = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float row_sum(float x) {
-  x += __shfl_xor(x, 16, 64);
-  return x + __shfl_xor(x, 32, 64);
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned v = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 __device__ __forceinline__ long long shfl64(long long x, int src) {
   const int lo = __shfl(static_cast<int>(x), src, 64);
   const int hi = __shfl(static_cast<int>(x >> 32), src, 64);
+  return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo);
+}
+
+__device__ __forceinline__ long long read_lane64(long long x, int src) {
+  const int lo = __builtin_amdgcn_readlane(static_cast<int>(x), src);
+  const int hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), src);
   return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo);
 }
 
@@ -80,32 +99,46 @@ struct TileRows {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// A wave-uniform pointer as it is, in scalar registers: without this the compiler adds the lanes' offsets
+// to its loop-invariant part and keeps a 64-bit vector address for each row.
+__device__ __forceinline__ GlobalBytes scalar_base(const void* p) {
+  unsigned long long bits = reinterpret_cast<uintptr_t>(p);
+  asm("" : "+s"(bits));
+  return (GlobalBytes)bits;
+}
+
 // A page-table entry at a wave-uniform place, by a scalar load.
 __device__ __forceinline__ int table_at(const int32_t* table, long long i) {
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   return *(Scalar)(reinterpret_cast<uintptr_t>(table + i));
 }
 
-template <typename T, int kDim, bool kFast, int kRowTiles>
+// One piece of a wave's range: tiles [first, end) of a segment (b, seg = kv head * chunks + chunk) of `tiles`;
+// none: end 0.
+template <typename T>
+struct AttendPiece {
+  int b, seg, len, n, chunks, tiles, first, end;
+  const T *kpool, *vpool;     // of the kv head
+  const int32_t* table;       // of the sequence
+};
+
+template <typename T, int kDim, bool kFast, int kRowTiles, bool kQueryLds>
 struct AttendWave {
   typedef Tile<T, kDim, kFast> L;
-  // Query operands that would take over kQueryRegs registers are read from LDS for each tile instead.
-  static constexpr bool kQueryLds = kRowTiles * L::kSteps > kQueryRegs / 4;
+  // kQueryLds: the query operands are read from LDS for each tile instead of staying in registers.
   static constexpr int kQueryTiles = kQueryLds ? 1 : kRowTiles;
 
   const KvArgs& c;
-  const T *kpool, *vpool;   // of the kv head
-  const int32_t* table;     // of the sequence
-  int page_shift, len, total, lane, col, g;
+  int page_shift, lane, col, g;
   float scale;
-  const u32x4 (*sh_q)[64];  // [row tile * steps][lane]
+  u32x4 (*sh_q)[64];        // [row tile * steps][lane]
   u32x4 q[kQueryTiles][L::kSteps];
   u32x4 kf[L::kSub][L::kSteps];
   unsigned vf[L::kRowsV][L::kWords];
   f32x4 o[kRowTiles][L::kOut];
   float m[kRowTiles], l[kRowTiles];
   int limit[kRowTiles];     // last slot that the lane's row sees
-  bool bad;
+  bool bad, bad_next;       // a page id outside the pool, in this piece and in the next one's first tile
 
   __device__ __forceinline__ explicit AttendWave(const KvArgs& args) : c(args) {}
 
@@ -120,105 +153,119 @@ struct AttendWave {
                : static_cast<int>(static_cast<unsigned>(slot) / static_cast<unsigned>(c.page_size));
   }
 
-  __device__ __forceinline__ Pages find(int tile) const {
+  __device__ __forceinline__ Pages find(const AttendPiece<T>& piece, int tile) const {
     Pages p;
+    const int last = piece.len + piece.n - 1;
     if constexpr (kFast) {
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub) {
         // (a group past the last slot takes the last slot's)
-        const int slot = min(tile * L::kKeys + 16 * sub, (total - 1) & ~15);
+        const int slot = min(tile * L::kKeys + 16 * sub, last & ~15);
         const int idx = uniform(page_index(slot));
         p.off[sub] = slot - idx * c.page_size;
-        p.page[sub] = table_at(table, idx);
+        p.page[sub] = table_at(piece.table, idx);
       }
     } else {
-      const int slot = min(tile * L::kKeys + (lane & (L::kKeys - 1)), total - 1);
+      const int slot = min(tile * L::kKeys + (lane & (L::kKeys - 1)), last);
       const int idx = page_index(slot);
       p.off[0] = slot - idx * c.page_size;
-      p.page[0] = table[idx];
+      p.page[0] = piece.table[idx];
     }
     return p;
   }
 
-  __device__ __forceinline__ Rows resolve(const Pages& p) {
+  __device__ __forceinline__ Rows resolve(const Pages& p, bool& wrong) {
     Rows r;
 #pragma unroll
     for (int x = 0; x < (kFast ? L::kSub : 1); ++x) {
       const bool good = static_cast<unsigned>(p.page[x]) < static_cast<unsigned>(c.num_pages);
-      bad = bad || !good;
+      wrong = wrong || !good;
       r.at[x] = (good ? p.page[x] : 0) * c.page_stride + p.off[x] * c.slot_stride;
     }
     return r;
   }
 
-  __device__ __forceinline__ void load_k(const Rows& r) {
+  __device__ __forceinline__ void load_k(const T* kpool, const Rows& r) {
 #pragma unroll
     for (int sub = 0; sub < L::kSub; ++sub) {
       if constexpr (kFast)
-        L::template load_row<true>(kf[sub], kpool + r.at[sub],
+        L::template load_row<true>(kf[sub], scalar_base(kpool + r.at[sub]),
                     static_cast<unsigned>(col) * static_cast<unsigned>(c.slot_stride), g, c.dim);
       else
-        L::template load_row<true>(kf[sub], kpool + shfl64(r.at[0], 16 * sub + col), 0u, g, c.dim);
+        L::template load_row<true>(kf[sub], (GlobalBytes)(kpool + shfl64(r.at[0], 16 * sub + col)), 0u, g, c.dim);
     }
   }
 
-  __device__ __forceinline__ void load_v(const Rows& r) {
+  __device__ __forceinline__ void load_v(const T* vpool, const Rows& r) {
 #pragma unroll
     for (int x = 0; x < L::kRowsV; ++x) {
       if constexpr (kFast)
-        L::template load_v<true>(vf[x], vpool + r.at[x / 4],
+        L::template load_v<true>(vf[x], scalar_base(vpool + r.at[x / 4]),
                   static_cast<unsigned>(4 * g + x % 4) * static_cast<unsigned>(c.slot_stride), col,
                   c.dim);
       else
-        L::template load_v<true>(vf[x], vpool + shfl64(r.at[0], L::slot_of(x / 4, x % 4, g)), 0u, col, c.dim);
+        L::template load_v<true>(vf[x], (GlobalBytes)(vpool + shfl64(r.at[0], L::slot_of(x / 4, x % 4, g))), 0u, col,
+                                 c.dim);
     }
   }
 
+  // All row tiles' and slot groups' chains side by side: a product waits for the one before it in its chain.
   __device__ __forceinline__ void scores(f32x4 (&p)[kRowTiles][L::kSub]) const {
 #pragma unroll
-    for (int t = 0; t < kRowTiles; ++t) {
-      u32x4 qt[L::kSteps];
+    for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-      for (int e = 0; e < L::kSteps; ++e)
-        qt[e] = kQueryLds ? sh_q[t * L::kSteps + e][lane] : q[kQueryLds ? 0 : t][e];
+      for (int sub = 0; sub < L::kSub; ++sub) p[t][sub] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int sub = 0; sub < L::kSub; ++sub) {
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < L::kSteps; ++e)
 #pragma unroll
-        for (int e = 0; e < L::kSteps; ++e) x = mma16(kf[sub][e], qt[e], x, T{});
-        p[t][sub] = x;
+      for (int t = 0; t < kRowTiles; ++t) {
+        const u32x4 qt = kQueryLds ? sh_q[t * L::kSteps + e][lane] : q[kQueryLds ? 0 : t][e];
+#pragma unroll
+        for (int sub = 0; sub < L::kSub; ++sub) p[t][sub] = mma16(kf[sub][e], qt, p[t][sub], T{});
+        if (kQueryLds && t == kRowTiles - 1) __builtin_amdgcn_sched_barrier(0);  // (one step's operands at a time)
       }
-    }
   }
 
-  // Scores to probabilities relative to the running maximum (kept in units of log2), which moves on.
+  // Scores to probabilities relative to a running base (in units of log2) that follows the row's maximum:
+  // it moves up when a score passes it by more than kSlack, so that probabilities stay under 2^kSlack
+  // (float16 holds 2^15) and the outputs are rescaled a few times a row, not with each new maximum.
   __device__ __forceinline__ void softmax(f32x4 (&p)[kRowTiles][L::kSub]) {
+    constexpr float kSlack = 8.f;
+    float top[kRowTiles];
+    bool up = false;
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
-      float top = p[t][0][0];
+      top[t] = p[t][0][0];
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, p[t][sub][x]);
-      top = fmaxf(m[t], row_max(top) * scale);
-      if (__any(top > m[t])) {
+        for (int x = 0; x < 4; ++x) top[t] = fmaxf(top[t], p[t][sub][x]);
+      top[t] = row_max(top[t]) * scale;
+      up = up || top[t] > m[t] + kSlack;
+    }
+    if (__any(up)) {
+#pragma unroll
+      for (int t = 0; t < kRowTiles; ++t) {
+        const float now = fmaxf(m[t], top[t]);
         // (no slot yet: m = -inf, and everything that it would scale is 0)
-        const float old = m[t] == -INFINITY ? 0.f : exp2_hw(m[t] - top);
+        const float old = m[t] == -INFINITY ? 0.f : exp2_hw(m[t] - now);
         l[t] *= old;
 #pragma unroll
         for (int x = 0; x < L::kOut; ++x) o[t][x] *= old;
-        m[t] = top;
+        m[t] = now;
       }
+    }
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
       const float base = m[t] == -INFINITY ? 0.f : m[t];
-      float sum = 0.f;
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          p[t][sub][x] = exp2_hw(fmaf(p[t][sub][x], scale, -base));
-          sum += p[t][sub][x];
-        }
-      l[t] += sum;
+        for (int x = 0; x < 4; ++x) p[t][sub][x] = exp2_hw(fmaf(p[t][sub][x], scale, -base));
+      // (added in pairs: a shorter chain, and the order is fixed)
+      f32x4 sum = p[t][0];
+      if constexpr (L::kSub == 2) sum += p[t][1];
+      l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
   }
 
@@ -281,7 +328,7 @@ struct AttendWave {
   // not see its slot, not even as 0 * value: a tile with such values (stale slots past the last one
   // included) is done in several products, first of the slots that every row sees, then slot by slot,
   // each added only to the rows that see it.
-  __device__ __forceinline__ void products_edge(const f32x4 (&p)[kRowTiles][L::kSub], int first) {
+  __device__ __forceinline__ void products_edge(const f32x4 (&p)[kRowTiles][L::kSub], int first, int len, int total) {
     bool finite = true;
 #pragma unroll
     for (int x = 0; x < L::kRowsV; ++x)
@@ -318,98 +365,186 @@ struct AttendWave {
     }
   }
 
-  // The wave's tiles first, first + step, .. before end.  The next tile's K is loaded while this one's
-  // scores become probabilities, its V after the products, and its pages are looked up one tile earlier.
-  __device__ __forceinline__ void walk(int tile, int end, int step) {
-    if (tile >= end) return;
-    Rows rows = resolve(find(tile));
-    load_k(rows);
-    load_v(rows);
-    Pages next = find(min(tile + step, end - 1));
-    const int whole_end = min(end, (len + 1) / L::kKeys);  // tiles of which every row sees every slot
+  // The next tile: of this piece, or past its end the next piece's first one (or none: the last again).
+  static __device__ __forceinline__ bool stays(const AttendPiece<T>& now, const AttendPiece<T>& next, int t) {
+    return t < now.end || next.end == 0;
+  }
+  __device__ __forceinline__ Pages ahead(const AttendPiece<T>& now, const AttendPiece<T>& next, int t) const {
+    if (stays(now, next, t)) return find(now, min(t, now.end - 1));
+    return find(next, next.first);
+  }
+
+  // Loads K of the tile after `tile`, looks up the pages of the one after that.
+  __device__ __forceinline__ Rows next_k(const AttendPiece<T>& now, const AttendPiece<T>& next, int tile,
+                                         Pages& pages) {
+    const bool inside = stays(now, next, tile + 1);
+    bool wrong = false;
+    const Rows rows = resolve(pages, wrong);
+    bad = bad || (wrong && inside);
+    bad_next = bad_next || (wrong && !inside);
+    const T* pool = now.kpool;
+    if (!inside) pool = next.kpool;
+    load_k(pool, rows);
+    pages = ahead(now, next, tile + 2);
+    return rows;
+  }
+  __device__ __forceinline__ void next_v(const AttendPiece<T>& now, const AttendPiece<T>& next, int tile,
+                                         const Rows& rows) {
+    const T* pool = now.vpool;
+    if (!stays(now, next, tile + 1)) pool = next.vpool;
+    load_v(pool, rows);
+  }
+
+  // The first tile of a piece before which there is no other one to load it ahead in.
+  __device__ __forceinline__ void enter(const AttendPiece<T>& piece) {
+    const Rows rows = resolve(find(piece, piece.first), bad);
+    load_k(piece.kpool, rows);
+    load_v(piece.vpool, rows);
+  }
+
+  // One row tile's rows of q of a piece.
+  __device__ __forceinline__ void load_q(u32x4 (&qt)[L::kSteps], const AttendArgs& a, const AttendPlan& plan,
+                                         int group, const AttendPiece<T>& p, int t) const {
+    const int h = p.seg / p.chunks, chunk = p.seg - h * p.chunks;
+    const int qrow = chunk * plan.rows + 16 * t + col, i = qrow / group;
+#pragma unroll
+    for (int x = 0; x < L::kSteps; ++x) qt[x] = u32x4{0, 0, 0, 0};
+    if (i < p.n)
+      L::template load_row<false>(
+          qt,
+          (GlobalBytes)(static_cast<const T*>(a.q) +
+                        (static_cast<long long>(p.b) * (a.K + 1) + i) * a.q_stride +
+                        static_cast<long long>(h * group + qrow - i * group) * c.dim),
+          0u, g, c.dim);
+  }
+
+  // No slot of a row tile's rows seen yet; the lane's row sees those up to `upto`.
+  __device__ __forceinline__ void clear(int t, int upto) {
+    m[t] = -INFINITY;
+    l[t] = 0.f;
+    limit[t] = upto;
+#pragma unroll
+    for (int x = 0; x < L::kOut; ++x) o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  __device__ __forceinline__ void mask(f32x4 (&p)[kRowTiles][L::kSub], int first) const {
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+      for (int sub = 0; sub < L::kSub; ++sub)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (first + L::slot_of(sub, x, g) > limit[t]) p[t][sub][x] = -INFINITY;
+  }
+
+  // The state before a piece's first tile.
+  __device__ __forceinline__ void begin(const AttendArgs& a, const AttendPlan& plan, int group,
+                                        const AttendPiece<T>& p) {
+    const int chunk = p.seg % p.chunks;
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      const int i = (chunk * plan.rows + 16 * t + col) / group;
+      clear(t, i < p.n ? p.len + i : -1);
+      if constexpr (kQueryLds) {
+        u32x4 qt[L::kSteps];
+        load_q(qt, a, plan, group, p, t);
+#pragma unroll
+        for (int x = 0; x < L::kSteps; ++x) sh_q[t * L::kSteps + x][lane] = qt[x];  // (read by this lane alone)
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // Query operands in registers are on their way while the piece before is written.
+  __device__ __forceinline__ void prefetch_q(const AttendArgs& a, const AttendPlan& plan, int group,
+                                             const AttendPiece<T>& p) {
+    if constexpr (!kQueryLds)
+#pragma unroll
+      for (int t = 0; t < kRowTiles; ++t) load_q(q[t], a, plan, group, p, t);
+  }
+
+  // A piece's tiles; K and V of the first are on their way already.  The next tile's K is loaded while
+  // this one's scores become probabilities, its V after the products, and its pages are looked up one
+  // tile earlier.  After the last tile comes the next piece's first one: its loads are in flight while
+  // this piece is written.
+  __device__ __forceinline__ void walk(const AttendPiece<T>& now, const AttendPiece<T>& next) {
+    int tile = now.first;
+    Pages pages = ahead(now, next, tile + 1);
     f32x4 p[kRowTiles][L::kSub];
-    for (; tile < whole_end; tile += step) {
+    const int whole_end = min(now.end, (now.len + 1) / L::kKeys);  // every row sees every slot
+    for (; tile < whole_end; ++tile) {
       scores(p);
       __builtin_amdgcn_sched_barrier(0);
-      rows = resolve(next);  // (past the last tile: that one again)
-      load_k(rows);
-      next = find(min(tile + 2 * step, end - 1));
+      const Rows rows = next_k(now, next, tile, pages);
       __builtin_amdgcn_sched_barrier(0);
       softmax(p);
       products(p);
       __builtin_amdgcn_sched_barrier(0);
-      load_v(rows);
+      next_v(now, next, tile, rows);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (; tile < end; tile += step) {
+    for (; tile < now.end; ++tile) {
       const int first = tile * L::kKeys;
       scores(p);
       __builtin_amdgcn_sched_barrier(0);
-      rows = resolve(next);
-      load_k(rows);
-      next = find(min(tile + 2 * step, end - 1));
+      const Rows rows = next_k(now, next, tile, pages);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-        for (int sub = 0; sub < L::kSub; ++sub)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (first + L::slot_of(sub, x, g) > limit[t]) p[t][sub][x] = -INFINITY;
+      mask(p, first);
       softmax(p);
-      products_edge(p, first);
+      products_edge(p, first, now.len, now.len + now.n);
       __builtin_amdgcn_sched_barrier(0);
-      load_v(rows);
+      next_v(now, next, tile, rows);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
-// Four elements from d on of an output row, and with the first its lse; a row past the last token is 0.
+// Four elements from d on of an output row, and with the first its lse.
 template <typename T>
-__device__ __forceinline__ void write_row(const AttendArgs& a, const KvArgs& c, long long row, bool used,
-                                          int d, f32x4 sum, float top, float total) {
-  const float inv = 1.f / total;
-  if (!used) sum = f32x4{0.f, 0.f, 0.f, 0.f};
-  else sum *= inv;
+__device__ __forceinline__ void write_row(const AttendArgs& a, const KvArgs& c, long long row, int d, f32x4 sum,
+                                          float top, float total) {
+  sum *= 1.f / total;
   T* out = static_cast<T*>(a.out) + row * c.dim + d;
   if constexpr (sizeof(T) == 2)
     *reinterpret_cast<u32x2*>(out) = u32x2{pack2<T>(sum[0], sum[1]), pack2<T>(sum[2], sum[3])};
   else
     *reinterpret_cast<f32x4*>(out) = sum;
   if (d == 0 && a.lse)
-    a.lse[row] = !used ? -INFINITY : top == -INFINITY ? __builtin_nanf("") : top * kLn2 + logf(total);
+    a.lse[row] = top == -INFINITY ? __builtin_nanf("") : top * kLn2 + logf(total);
 }
 
-// Adds up the parts of a cut segment: workgroup (w, y) the rows 16 y .. of the one whose first part
-// workgroup w of the split holds.  dim / 4 lanes share a row, so a wave loads 256 / dim parts' worth at once,
-// four of them ahead.
+// Adds up the parts of a cut segment: workgroups (w, *) those of the one whose first part workgroup w of
+// the split holds.  kDim / 4 lanes take a row's part; with few parts such groups take different rows, with
+// many they take parts of one row and are added up in LDS.
 template <typename T, int kDim>
-__global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs a, KvArgs c,
-                                                                     AttendPlan plan) {
-  constexpr int kLanes = kDim / 4;                    // lanes of a row
-  constexpr int kRowsOnce = kAttendThreads / kLanes;  // rows at once
+__global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(AttendArgs a, KvArgs c, AttendPlan plan) {
+  constexpr int kLanes = kDim / 4;
+  constexpr int kTeams = kJoinThreads / kLanes;
+  constexpr int kAhead = 8;
+  __shared__ f32x4 sh_o[kTeams][kLanes];
+  __shared__ float sh_m[kTeams], sh_l[kTeams];
   const int w = blockIdx.x;
   const CutSegment cut = plan.cut[w];
   if (cut.parts == 0) return;
-  const RoundRows r = round_rows(c, a.num_draft, a.kv_len, cut.b, a.K);
   const int group = a.q_heads / c.heads;
-  const int h = cut.seg / plan.chunks, chunk = cut.seg - h * plan.chunks;
-  const int d = threadIdx.x % kLanes * 4;
-  const int end = min(plan.rows, (a.K + 1) * group - chunk * plan.rows);
-  for (int local = blockIdx.y * kRowsOnce + threadIdx.x / kLanes; local < end; local += gridDim.y * kRowsOnce) {
+  const int chunks = chunks_of(cut.n, group, plan.rows);
+  const int h = cut.seg / chunks, chunk = cut.seg - h * chunks;
+  const int team = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  const int end = min(plan.rows, cut.n * group - chunk * plan.rows);
+  const bool by_part = cut.parts > kAhead;
+  const int rows_once = by_part ? 1 : kTeams, part_step = by_part ? kTeams : 1;
+  for (int row = blockIdx.y * rows_once; row < end; row += gridDim.y * rows_once) {
+    const int local = by_part ? row : row + team;
     const int qrow = chunk * plan.rows + local, i = qrow / group;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float top = -INFINITY, sum = 0.f;
-    if (i < r.n) {
-      constexpr int kAhead = 8;
-      for (int p = 0; p < cut.parts; p += kAhead) {
+    if (local < end) {
+      for (int p = by_part ? team : 0; p < cut.parts; p += kAhead * part_step) {
         f32x4 x[kAhead];
         float m[kAhead], l[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
-          const int q = min(p + e, cut.parts - 1);
-          const long long at = (2LL * (w + q) + (q == 0 ? cut.first_slot : 0)) * plan.rows + local;
+          const int part = min(p + e * part_step, cut.parts - 1);
+          const long long at = (2LL * (w + part) + (part == 0 ? 1 : 0)) * plan.rows + local;
           x[e] = *reinterpret_cast<const f32x4*>(plan.part_o + at * kDim + d);
           m[e] = plan.part_m[at];
           l[e] = plan.part_l[at];
@@ -423,7 +558,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs 
         sum *= old;
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
-          if (p + e >= cut.parts) break;
+          if (p + e * part_step >= cut.parts) break;
           const float f = exp2_hw(m[e] - base);
           o += x[e] * f;
           sum += l[e] * f;
@@ -431,246 +566,544 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs 
         top = now;
       }
     }
-    if (d < c.dim)
-      write_row<T>(a, c, (static_cast<long long>(cut.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
-                   i < r.n, d, o, top, sum);
+    if (by_part) {
+      sh_o[team][d / 4] = o;
+      if (d == 0) {
+        sh_m[team] = top;
+        sh_l[team] = sum;
+      }
+      __syncthreads();
+      top = -INFINITY;
+      for (int t = 0; t < kTeams; ++t) top = fmaxf(top, sh_m[t]);
+      const float base = top == -INFINITY ? 0.f : top;
+      o = f32x4{0.f, 0.f, 0.f, 0.f};
+      sum = 0.f;
+      for (int t = 0; t < kTeams; ++t) {
+        const float f = exp2_hw(sh_m[t] - base);
+        o += sh_o[t][d / 4] * f;
+        sum += sh_l[t] * f;
+      }
+      __syncthreads();
+    }
+    if (local < end && d < c.dim && (!by_part || team == 0))
+      write_row<T>(a, c,
+                   (static_cast<long long>(cut.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
+                   d, o, top, sum);
   }
 }
 
-// kFast: head_dim is kDim, pages are whole groups of 16 slots and 16 slots lie within 2^32 bytes.
-template <typename T, int kDim, bool kFast, int kRowTiles, int kOccupancy>
-__global__ __launch_bounds__(kAttendThreads, kOccupancy) void attend_split_kernel(AttendArgs a, KvArgs c,
-                                                                                  AttendPlan plan) {
-  typedef Tile<T, kDim, kFast> L;
-  typedef AttendWave<T, kDim, kFast, kRowTiles> Wave;
-  constexpr int kPad = kDim + 4;
-  constexpr int kTilesUnit = kUnit / L::kKeys;
-  __shared__ float sh_o[kAttendWaves][16][kPad];
-  __shared__ float sh_m[kAttendWaves][kRowTiles * 16], sh_l[kAttendWaves][kRowTiles * 16];
-  __shared__ float sh_top[kAttendWaves][kRowTiles * 16], sh_sum[kAttendWaves][kRowTiles * 16];
-  __shared__ u32x4 sh_q[Wave::kQueryLds ? kAttendWaves : 1][Wave::kQueryLds ? kRowTiles * L::kSteps : 1][64];
-  __shared__ long long sh_scan[kAttendWaves], sh_before;
-  __shared__ int sh_b;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int col = lane & 15, g = lane >> 4;
-  const int group = a.q_heads / c.heads;
-  const int segs = c.heads * plan.chunks;  // segments of a sequence
-  // Units before each sequence: every thread sums a run of sequences, then a scan over the threads.
-  const int per = (a.B + kAttendThreads - 1) / kAttendThreads;
-  const int run0 = min(a.B, tid * per), run1 = min(a.B, run0 + per);
+// The piece of a range that begins with tile `first` of a segment and has `left` tiles at most.
+template <typename T, int kKeys>
+__device__ __forceinline__ AttendPiece<T> make_piece(const KvArgs& c, const AttendPlan& plan, int group, int b,
+                                                     int seg, int len, int n, int first, long long left) {
+  AttendPiece<T> p;
+  p.b = b;
+  p.seg = seg;
+  p.len = len;
+  p.n = n;
+  p.chunks = chunks_of(n, group, plan.rows);
+  p.tiles = tiles_of<kKeys>(len, n);
+  p.first = first;
+  p.end = static_cast<int>(min(static_cast<long long>(p.tiles), first + left));
+  const int h = seg / p.chunks;
+  p.kpool = reinterpret_cast<const T*>(c.k) + h * c.head_stride;
+  p.vpool = reinterpret_cast<const T*>(c.v) + h * c.head_stride;
+  p.table = c.table + static_cast<long long>(b) * c.max_pages;
+  return p;
+}
+
+// A wave's (or workgroup's) range, and the piece of a segment that it begins with.
+struct RangeStart {
+  long long total, begin, end;
+  int w, b, len, n, seg, first;
+};
+
+// Every wave finds its own: `waves` ranges a workgroup, this one's number is `wave`.
+template <int kKeys>
+__device__ __forceinline__ RangeStart range_start(const AttendArgs& a, const KvArgs& c, const AttendPlan& plan,
+                                                  int group, int lane, int waves, int wave) {
+  // Tiles before each sequence: every lane sums a run of sequences, then a scan over the lanes.
+  const int per = (a.B + 63) / 64;
+  const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
   long long mine = 0;
-  for (int b = run0; b < run1; ++b) mine += units_of(round_rows(c, a.num_draft, a.kv_len, b, a.K));
+  RoundRows r{};
+  for (int b = run0; b < run1; ++b) {
+    r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
+    mine += work_of<kKeys>(r, c.heads, group, plan.rows);
+  }
   long long upto = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const long long y = shfl64(upto, max(lane - off, 0));
     if (lane >= off) upto += y;
   }
-  if (lane == 63) sh_scan[wave] = upto;
-  __syncthreads();
-  long long all = 0;
-  for (int x = 0; x < kAttendWaves; ++x) {
-    if (x < wave) upto += sh_scan[x];
-    all += sh_scan[x];
+  RangeStart s{};
+  s.total = read_lane64(upto, 63);
+  // Neighbouring ranges go to one XCD (workgroups are dealt to the 8 XCDs in turn), so that row chunks of
+  // the same slots meet in its L2; too few tiles for that go round all XCDs.
+  const int wg = s.total >> plan.log_ranges == 0
+                     ? static_cast<int>(blockIdx.x)
+                     : static_cast<int>(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  s.w = wg * waves + wave;
+  s.begin = range_begin(s.w, s.total, plan.log_ranges);
+  s.end = range_begin(s.w + 1, s.total, plan.log_ranges);
+  if (s.begin >= s.end) return s;
+  // The sequence that holds tile `begin`: the lane whose run does, then along its run.
+  const int owner = __builtin_ctzll(__ballot(mine > 0 && s.begin < upto));
+  long long before = read_lane64(upto - mine, owner);
+  s.b = uniform(owner * per);
+  s.len = __builtin_amdgcn_readlane(r.len, owner);
+  s.n = __builtin_amdgcn_readlane(r.n, owner);
+  for (; per > 1; ++s.b) {
+    const RoundRows x = round_rows(c, a.num_draft, a.kv_len, s.b, a.K);
+    s.len = uniform(x.len);
+    s.n = uniform(x.n);
+    const long long work = work_of<kKeys>(x, c.heads, group, plan.rows);
+    if (s.begin < before + work) break;
+    before += work;
   }
-  long long before = upto - mine;
-  const long long total_units = all * segs;
-  const int groups = active_groups(total_units, plan.groups);
-  // Neighbouring ranges go to workgroups of one XCD (workgroups are dealt to the 8 XCDs in turn), so
-  // that row chunks of the same slots meet in its L2; too few units for that go round all XCDs.
-  const int w = groups == plan.groups
-                    ? static_cast<int>(blockIdx.x % 8 * (plan.groups / 8) + blockIdx.x / 8)
-                    : static_cast<int>(blockIdx.x);
-  // Sequences without units are invalid: their rows are NaN.
+  // (a sequence has under 2^28 tiles; `inside` is under 2^53, so the quotient's floor is exact)
+  const int tiles = tiles_of<kKeys>(s.len, s.n);
+  const long long inside = s.begin - before;
+  s.seg = uniform(static_cast<int>(static_cast<double>(inside) / static_cast<double>(tiles)));
+  s.first = uniform(static_cast<int>(inside - static_cast<long long>(s.seg) * tiles));
+  return s;
+}
+
+// Rows past the last new token are 0, those of an invalid sequence NaN.
+template <typename T>
+__device__ __forceinline__ void fill_unused_rows(const AttendArgs& a, const KvArgs& c) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const RoundRows r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
-    if (r.n > 0) continue;
     const long long row = static_cast<long long>(b) * (a.K + 1) * a.q_heads;
-    const long long bad = static_cast<long long>(r.rows) * a.q_heads;
-    const long long rows = (a.K + 1LL) * a.q_heads;
+    const long long rows = (a.K + 1LL) * a.q_heads, wrong = static_cast<long long>(r.rows) * a.q_heads;
     T* out = static_cast<T*>(a.out) + row * c.dim;
-    for (long long x = tid; x < rows * c.dim; x += kAttendThreads)
-      out[x] = from_float<T>(x < bad * c.dim ? __builtin_nanf("") : 0.f);
-    for (long long x = tid; a.lse && x < rows; x += kAttendThreads)
-      a.lse[row + x] = x < bad ? __builtin_nanf("") : -INFINITY;
+    const long long from = static_cast<long long>(r.n) * a.q_heads;
+    for (long long x = from * c.dim + threadIdx.x; x < rows * c.dim; x += blockDim.x)
+      out[x] = from_float<T>(x < wrong * c.dim ? __builtin_nanf("") : 0.f);
+    for (long long x = from + threadIdx.x; a.lse && x < rows; x += blockDim.x)
+      a.lse[row + x] = x < wrong ? __builtin_nanf("") : -INFINITY;
   }
-  if (tid == 0) plan.cut[w].parts = 0;
-  if (w >= groups) return;
-  const long long begin = range_begin(w, total_units, groups);
-  const long long end = range_begin(w + 1, total_units, groups);
-  if (mine > 0 && before * segs <= begin && begin < (before + mine) * segs) {
-    int b = run0;
-    for (;; ++b) {
-      const long long u = units_of(round_rows(c, a.num_draft, a.kv_len, b, a.K));
-      if (begin < (before + u) * segs) break;
-      before += u;
-    }
-    sh_b = b;
-    sh_before = before;
-  }
-  __syncthreads();
-  int b = uniform(sh_b);
-  RoundRows r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
-  // From here on 32 bits do: a sequence has under 2^24 units, and a range that starts in one of its
-  // segments is cut at the segment's end piece by piece.
-  int units = static_cast<int>(units_of(r));
-  const long long inside = begin - sh_before * segs;
-  int seg = uniform(static_cast<int>(inside / units));
-  int at = uniform(static_cast<int>(inside - static_cast<long long>(seg) * units));
-  long long left = end - begin;
-  int slot_of_part = 0;
+}
 
-  const int rw = wave % plan.row_waves, kw = wave / plan.row_waves;
-  const int key_waves = kAttendWaves / plan.row_waves;
+// What a wave leaves of a segment that it has a part of.
+struct PartNote {
+  int b, seg, n, chunks;
+  bool any, begins, ends;
+  long long segment_end;  // of one that begins: the tile after its last
+};
+
+// Waves a SIMD that the registers of the split kernel are planned for.
+template <typename T>
+constexpr int split_occupancy(int dim, bool fast, int row_tiles) {
+  return dim == 256 || (dim == 128 && row_tiles == 2 && (!fast || sizeof(T) == 4)) ? 1 : 2;
+}
+
+// A wave works through its range on its own: none waits for another until all are done.  Then a workgroup of
+// several waves adds up in LDS the segments that its waves have cut between them.  kFast: head_dim is kDim,
+// pages are whole groups of 16 slots and 16 slots lie within 2^32 bytes.
+template <typename T, int kDim, bool kFast, int kRowTiles, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTiles)) void attend_split_kernel(
+    AttendArgs a, KvArgs c, AttendPlan plan) {
+  typedef Tile<T, kDim, kFast> L;
+  // (where the LDS does not hold parts and they would take over 32 registers)
+  constexpr bool kQueryLds = kWaves == 1 && kRowTiles * L::kSteps > 8;
+  typedef AttendWave<T, kDim, kFast, kRowTiles, kQueryLds> Wave;
+  constexpr int kRows = 16 * kRowTiles, kPad = kDim + 4;
+  __shared__ u32x4 sh_q[kQueryLds ? kRowTiles * L::kSteps : 1][64];
+  // (dynamic, so that the compiler plans registers for two waves a SIMD: with one it keeps the outputs in
+  // accumulation registers and moves them back and forth for every tile)
+  extern __shared__ float sh_parts[];
+  auto sh_o = [&](int note, int row, int d) __attribute__((always_inline)) {
+    return reinterpret_cast<f32x4*>(sh_parts + (note * kRows + row) * kPad + d);
+  };
+  __shared__ float sh_m[2 * kWaves][kRows], sh_l[2 * kWaves][kRows];
+  __shared__ PartNote sh_note[2 * kWaves];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int group = a.q_heads / c.heads;
+  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, kWaves, wave);
+  const int w = at.w, wg = w / kWaves;
+  const long long begin = at.begin, end = at.end, total = at.total;
+  fill_unused_rows<T>(a, c);
+  if (threadIdx.x == 0) plan.cut[wg].parts = 0;
+  if (kWaves > 1 && lane < 2) sh_note[2 * wave + lane].any = false;
+  if (begin < end) {
   Wave s(c);
   s.page_shift = plan.page_shift;
   s.lane = lane;
   s.col = col;
   s.g = g;
   s.scale = plan.scale_log2;
-  s.sh_q = sh_q[Wave::kQueryLds ? wave : 0];
+  s.sh_q = sh_q;
+  s.bad = s.bad_next = false;
 
-  while (left > 0) {
-    // One piece: units [at, stop) of segment (b, h, chunk).
-    const int len = uniform(r.len), n = uniform(r.n);
-    const int stop = uniform(static_cast<int>(min(static_cast<long long>(units), at + left)));
-    const int h = seg / plan.chunks, chunk = seg - h * plan.chunks;
-    const int row0 = chunk * plan.rows + rw * 16 * kRowTiles;
-    s.len = len;
-    s.total = len + n;
-    s.kpool = reinterpret_cast<const T*>(c.k) + h * c.head_stride;
-    s.vpool = reinterpret_cast<const T*>(c.v) + h * c.head_stride;
-    s.table = c.table + static_cast<long long>(b) * c.max_pages;
-    s.bad = false;
-#pragma unroll
-    for (int t = 0; t < kRowTiles; ++t) {
-      const int qrow = row0 + 16 * t + col;
-      const int i = qrow / group;
-      s.m[t] = -INFINITY;
-      s.l[t] = 0.f;
-      s.limit[t] = i < n ? len + i : -1;
-#pragma unroll
-      for (int x = 0; x < L::kOut; ++x) s.o[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-      u32x4 qt[L::kSteps];
-#pragma unroll
-      for (int x = 0; x < L::kSteps; ++x) qt[x] = u32x4{0, 0, 0, 0};
-      if (i < n)
-        L::template load_row<false>(qt,
-                    static_cast<const T*>(a.q) + (static_cast<long long>(b) * (a.K + 1) + i) * a.q_stride +
-                        static_cast<long long>(h * group + qrow - i * group) * c.dim,
-                    0u, g, c.dim);
-#pragma unroll
-      for (int x = 0; x < L::kSteps; ++x) {
-        if constexpr (Wave::kQueryLds)
-          sh_q[wave][t * L::kSteps + x][lane] = qt[x];  // (read back by this lane alone)
-        else
-          s.q[t][x] = qt[x];
+  long long left = end - begin;
+  AttendPiece<T> now = make_piece<T, L::kKeys>(c, plan, group, at.b, at.seg, at.len, at.n, at.first, left), next;
+  left -= now.end - now.first;
+  s.enter(now);
+  s.prefetch_q(a, plan, group, now);
+
+  for (;;) {
+    const bool more = left > 0;
+    next = now;
+    next.end = 0;
+    if (more) {
+      int nb = now.b, seg = now.seg + 1, nlen = now.len, nn = now.n;
+      if (seg == c.heads * now.chunks) {
+        seg = 0;
+        do {
+          const RoundRows x = round_rows(c, a.num_draft, a.kv_len, ++nb, a.K);
+          nlen = uniform(x.len);
+          nn = uniform(x.n);
+        } while (nn == 0);
       }
+      next = make_piece<T, L::kKeys>(c, plan, group, nb, seg, nlen, nn, 0, left);
+      left -= next.end;
     }
-    if (row0 < n * group)  // (a wave without rows has nothing to read)
-      s.walk(at * kTilesUnit + kw, min(stop * kTilesUnit, (len + n + L::kKeys - 1) / L::kKeys),
-             key_waves);
+    s.begin(a, plan, group, now);
+    s.walk(now, next);
+    if (more) s.prefetch_q(a, plan, group, next);
 
-    // Join the waves that split the slots, 16 rows a round, and write the segment's rows or, if another
-    // workgroup holds the rest of it, this piece's part.
-    const bool whole = at == 0 && stop == units;
+    // The rows, or if other ranges hold the rest of the segment this piece's part of them.
+    const bool begins = now.first == 0, ends = now.end == now.tiles, whole = begins && ends;
+    const int h = now.seg / now.chunks, chunk = now.seg - h * now.chunks;
+    const int slot = begins ? 1 : 0;
+    if (kWaves > 1 && !whole && lane == 0)
+      sh_note[2 * wave + slot] = PartNote{now.b,  now.seg, now.n, now.chunks,
+                                             true,   begins,  ends,  end - now.end + now.tiles};
+    if (kWaves == 1 && begins && !ends && lane == 0)
+      plan.cut[wg] = CutSegment{range_of(end - now.end + now.tiles - 1, total, plan.log_ranges) - wg + 1,
+                                now.b, now.seg, now.n};
     const bool bad = __any(s.bad);
+    int id = threadIdx.x & 63;  // (volatile: addresses are made here, not kept through the walk)
+    asm volatile("" : "+v"(id));
+    const int col = id & 15, g = id >> 4;
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
-      s.l[t] = row_sum(s.l[t]);
+      const int local = 16 * t + col, qrow = chunk * plan.rows + local, i = qrow / group;
+      float sum = row_sum(s.l[t]), top = s.m[t];
       if (bad) {  // a page id outside the pool: the rows' sums are NaN, whatever else they hold
-        s.l[t] = __builtin_nanf("");
-        if (s.m[t] == -INFINITY) s.m[t] = 0.f;
+        sum = __builtin_nanf("");
+        if (top == -INFINITY) top = 0.f;
       }
-      if (g == 0) {
-        sh_m[wave][16 * t + col] = s.m[t];
-        sh_l[wave][16 * t + col] = s.l[t];
-      }
-    }
-    __syncthreads();
-    const long long part = 2LL * w + slot_of_part;
-#pragma unroll
-    for (int t = 0; t < kRowTiles; ++t) {
-      float top = -INFINITY;
-      for (int x = 0; x < key_waves; ++x) top = fmaxf(top, sh_m[x * plan.row_waves + rw][16 * t + col]);
-      const float base = top == -INFINITY ? 0.f : top;
-      if (kw == 0 && g == 0) {
-        float sum = 0.f;
-        for (int x = 0; x < key_waves; ++x)
-          sum += sh_l[x * plan.row_waves + rw][16 * t + col] *
-                 exp2_hw(sh_m[x * plan.row_waves + rw][16 * t + col] - base);
-        sh_top[rw][16 * t + col] = top;
-        sh_sum[rw][16 * t + col] = sum;
-      }
-      const float f = exp2_hw(s.m[t] - base);
+      if (i >= now.n) continue;
+      const long long row =
+          (static_cast<long long>(now.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group;
+      const long long part_row = (2LL * wg + slot) * plan.rows + local;
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < L::kOut; y += 4)
-          *reinterpret_cast<f32x4*>(&sh_o[wave][col][L::kChunk * (4 * g + x) + y]) =
-              f32x4{s.o[t][y][x], s.o[t][y + 1][x], s.o[t][y + 2][x], s.o[t][y + 3][x]} * f;
-      __syncthreads();
-      constexpr int kVecs = 16 * kDim / 4;
-      for (int idx = tid; idx < plan.row_waves * kVecs; idx += kAttendThreads) {
-        const int rwi = idx / kVecs, rr = idx % kVecs / (kDim / 4), d = idx % (kDim / 4) * 4;
-        f32x4 sum = *reinterpret_cast<f32x4*>(&sh_o[rwi][rr][d]);
-        for (int x = 1; x < key_waves; ++x)
-          sum += *reinterpret_cast<f32x4*>(&sh_o[x * plan.row_waves + rwi][rr][d]);
-        const int local = rwi * 16 * kRowTiles + 16 * t + rr;
-        const float rtop = sh_top[rwi][16 * t + rr], rsum = sh_sum[rwi][16 * t + rr];
-        if (whole) {
+        for (int y = 0; y < L::kOut; y += 4) {
+          const int d = L::kChunk * (4 * g + x) + y;
+          const f32x4 four = {s.o[t][y][x], s.o[t][y + 1][x], s.o[t][y + 2][x], s.o[t][y + 3][x]};
+          if (whole) {
+            if (d < c.dim) write_row<T>(a, c, row, d, four, top, sum);
+          } else if (kWaves > 1) {
+            *sh_o(2 * wave + slot, local, d) = four;
+          } else {
+            *reinterpret_cast<f32x4*>(plan.part_o + part_row * kDim + d) = four;
+          }
+          __builtin_amdgcn_sched_barrier(0);  // (few copies of the outputs at a time)
+        }
+      if (!whole && g == 0) {
+        (kWaves > 1 ? sh_m[2 * wave + slot][local] : plan.part_m[part_row]) = top;
+        (kWaves > 1 ? sh_l[2 * wave + slot][local] : plan.part_l[part_row]) = sum;
+      }
+    }
+    if (!more) break;
+    now = next;
+    s.bad = s.bad_next;
+    s.bad_next = false;
+  }
+  }
+  if constexpr (kWaves > 1) {
+    __syncthreads();
+    // Neighbouring parts of one segment, in order: a wave's part that begins nothing comes first.
+    for (int x = 0; x < 2 * kWaves;) {
+      const PartNote first = sh_note[x];
+      if (!first.any) {
+        ++x;
+        continue;
+      }
+      int last = x;
+      bool ends = first.ends;
+      for (int y = x + 1; y < 2 * kWaves && !ends; ++y)
+        if (sh_note[y].any) {
+          last = y;
+          ends = sh_note[y].ends;
+        }
+      const int h = first.seg / first.chunks, chunk = first.seg - h * first.chunks;
+      const int used = min(kRows, first.n * group - chunk * plan.rows);
+      for (int idx = threadIdx.x; idx < used * (kDim / 4); idx += 64 * kWaves) {
+        const int local = idx / (kDim / 4), d = idx % (kDim / 4) * 4;
+        float top = -INFINITY;
+        for (int y = x; y <= last; ++y)
+          if (sh_note[y].any) top = fmaxf(top, sh_m[y][local]);
+        const float base = top == -INFINITY ? 0.f : top;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        float sum = 0.f;
+        for (int y = x; y <= last; ++y)
+          if (sh_note[y].any) {
+            const float f = exp2_hw(sh_m[y][local] - base);
+            o += *sh_o(y, local, d) * f;
+            sum += sh_l[y][local] * f;
+          }
+        if (first.begins && ends) {
           const int qrow = chunk * plan.rows + local, i = qrow / group;
-          if (i <= a.K && d < c.dim)
-            write_row<T>(a, c, (static_cast<long long>(b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
-                         i < n, d, sum, rtop, rsum);
-        } else if (chunk * plan.rows + local < n * group) {
-          const long long at_row = part * plan.rows + local;
-          *reinterpret_cast<f32x4*>(plan.part_o + at_row * kDim + d) = sum;
+          if (d < c.dim)
+            write_row<T>(a, c,
+                         (static_cast<long long>(first.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group,
+                         d, o, top, sum);
+        } else {
+          const long long row = (2LL * wg + (first.begins ? 1 : 0)) * plan.rows + local;
+          *reinterpret_cast<f32x4*>(plan.part_o + row * kDim + d) = o;
           if (d == 0) {
-            plan.part_m[at_row] = rtop;
-            plan.part_l[at_row] = rsum;
+            plan.part_m[row] = top;
+            plan.part_l[row] = sum;
           }
         }
       }
-      __syncthreads();
-    }
-    if (at == 0 && stop < units && tid == 0) {
-      const int last = owner_of(begin + (end - begin - left) + units - 1, total_units, groups);
-      plan.cut[w] = CutSegment{last - w + 1, b, seg, slot_of_part};
-    }
-    slot_of_part = 1;
-    left -= stop - at;
-    at = 0;
-    if (left > 0 && ++seg == segs) {
-      seg = 0;
-      do {
-        r = round_rows(c, a.num_draft, a.kv_len, ++b, a.K);
-        units = uniform(static_cast<int>(units_of(r)));
-      } while (units == 0);
+      if (first.begins && !ends && threadIdx.x == 0) {  // (it ends the workgroup's range)
+        plan.cut[wg] = CutSegment{range_of(first.segment_end - 1, total, plan.log_ranges) / kWaves - wg + 1,
+                                  first.b, first.seg, first.n};
+      }
+      x = last + 1;
     }
   }
 }
 
-template <typename T, int kDim>
-void launch_join(const AttendArgs& a, const KvArgs& c, const AttendPlan& p) {
-  constexpr int kRowsOnce = kAttendThreads / (kDim / 4);
-  const int rows = p.rows < (a.K + 1) * (a.q_heads / c.heads) ? p.rows : (a.K + 1) * (a.q_heads / c.heads);
-  const dim3 grid(p.groups, (rows + kRowsOnce - 1) / kRowsOnce);
-  attend_join_kernel<T, kDim><<<grid, kAttendThreads, 0, a.stream>>>(a, c, p);
+// The same for many rows: waves with 16 or 32 rows each share every tile of K and V through LDS; the next tile is
+// on its way in registers while this one is computed on.  A tile lies in LDS operand by operand, 64 lanes x 16
+// bytes as the matrix instructions take them, so that it is written and read in order, without bank conflicts.
+// (Two tiles a barrier took 650 us for 64 rows over 64 x 8-16k slots where one takes 596; two tiles ahead in
+// registers 648; 16 rows a wave 648 where 64 rows in one wave took 588-670.)
+template <typename T, int kDim, bool kFast, int kRowTiles, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, kDim == 256 ? 1 : 2) void attend_wide_kernel(AttendArgs a, KvArgs c,
+                                                                                       AttendPlan plan) {
+  typedef Tile<T, kDim, kFast> L;
+  typedef AttendWave<T, kDim, kFast, kRowTiles, false> Wave;
+  constexpr int kStepsK = L::kSub * L::kSteps;     // K operands a tile, a wave's share of them to load
+  constexpr int kStepsV = L::kRowsV * L::kLoadsV;  // V loads a tile, likewise
+  constexpr int kMineK = kStepsK / kWaves, kMineV = kStepsV / kWaves;
+  typedef typename L::LoadV VecV;
+  extern __shared__ float sh_parts[];
+  u32x4* sh_k = reinterpret_cast<u32x4*>(sh_parts);               // [2][kStepsK][64]
+  VecV* sh_v = reinterpret_cast<VecV*>(sh_k + 2 * kStepsK * 64);  // [2][kStepsV][64]
+  __shared__ int sh_bad[kWaves];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int group = a.q_heads / c.heads;
+  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, 1, 0);
+  const int wg = at.w;
+  fill_unused_rows<T>(a, c);
+  if (threadIdx.x == 0) plan.cut[wg].parts = 0;
+  if (at.begin >= at.end) return;
+
+  Wave s(c);
+  s.page_shift = plan.page_shift;
+  s.lane = lane;
+  s.col = col;
+  s.g = g;
+  s.scale = plan.scale_log2;
+  s.bad = false;
+  long long left = at.end - at.begin;
+  AttendPiece<T> now = make_piece<T, L::kKeys>(c, plan, group, at.b, at.seg, at.len, at.n, at.first, left);
+  const int sub = L::kSub == 2 ? 2 * wave / kWaves : 0;  // the 16-slot group of all that this wave loads
+  const int step_k = wave * kMineK % L::kSteps, step_v = wave * kMineV;
+
+  for (;;) {
+    left -= now.end - now.first;
+    const int h = now.seg / now.chunks, chunk = now.seg - h * now.chunks;
+    const int wave_row = chunk * plan.rows + 16 * kRowTiles * wave;
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      const int qrow = wave_row + 16 * t + col, i = qrow / group;
+      s.clear(t, i < now.n ? now.len + i : -1);
+#pragma unroll
+      for (int x = 0; x < L::kSteps; ++x) s.q[t][x] = u32x4{0, 0, 0, 0};
+      if (i < now.n)
+        L::template load_row<false>(
+            s.q[t],
+            (GlobalBytes)(static_cast<const T*>(a.q) +
+                          (static_cast<long long>(now.b) * (a.K + 1) + i) * a.q_stride +
+                          static_cast<long long>(h * group + qrow - i * group) * c.dim),
+            0u, g, c.dim);
+    }
+
+    // The wave's part of the tile on its way, in registers, and where the next one's rows lie.
+    u32x4 mine_k[kMineK];
+    VecV mine_v[kMineV];
+    int page[kFast ? 1 : 1 + kMineV], off[kFast ? 1 : 1 + kMineV];
+    const int last_slot = now.len + now.n - 1;
+    auto find = [&](int tile) __attribute__((always_inline)) {
+      const int base = min(tile, now.end - 1) * L::kKeys;  // (past the end: the last tile again)
+      if constexpr (kFast) {
+        const int slot = min(base + 16 * sub, last_slot & ~15);
+        const int idx = uniform(s.page_index(slot));
+        off[0] = slot - idx * c.page_size;
+        page[0] = table_at(now.table, idx);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 1 + kMineV; ++y) {
+          const int v = (step_v + y - 1) / L::kLoadsV;
+          const int slot = min(base + (y == 0 ? 16 * sub + col : 16 * (v / 4) + 4 * g + v % 4), last_slot);
+          const int idx = s.page_index(slot);
+          off[y] = slot - idx * c.page_size;
+          page[y] = now.table[idx];
+        }
+      }
+    };
+    auto row_of = [&](int y) __attribute__((always_inline)) {
+      const bool good = static_cast<unsigned>(page[y]) < static_cast<unsigned>(c.num_pages);
+      s.bad = s.bad || !good;
+      return (good ? page[y] : 0) * c.page_stride + off[y] * c.slot_stride;
+    };
+    auto fetch = [&]() __attribute__((always_inline)) {
+      const long long k_row = row_of(0);
+#pragma unroll
+      for (int y = 0; y < kMineK; ++y) {
+        if constexpr (kFast)
+          mine_k[y] = L::template load_step<true>(
+              scalar_base(now.kpool + k_row), static_cast<unsigned>(col) * static_cast<unsigned>(c.slot_stride),
+              step_k + y, g, c.dim);
+        else
+          mine_k[y] = L::template load_step<true>((GlobalBytes)(now.kpool + k_row), 0u, step_k + y, g, c.dim);
+      }
+#pragma unroll
+      for (int y = 0; y < kMineV; ++y) {
+        const int v = (step_v + y) / L::kLoadsV, z = (step_v + y) % L::kLoadsV;
+        if constexpr (kFast)
+          mine_v[y] = L::template load_v_step<true>(
+              scalar_base(now.vpool + k_row),
+              static_cast<unsigned>(4 * g + v % 4) * static_cast<unsigned>(c.slot_stride), z, col, c.dim);
+        else
+          mine_v[y] = L::template load_v_step<true>((GlobalBytes)(now.vpool + row_of(1 + y)), 0u, z, col, c.dim);
+      }
+    };
+    auto put = [&](int buffer) __attribute__((always_inline)) {
+#pragma unroll
+      for (int y = 0; y < kMineK; ++y)
+        sh_k[(buffer * kStepsK + wave * kMineK + y) * 64 + lane] = mine_k[y];
+#pragma unroll
+      for (int y = 0; y < kMineV; ++y) sh_v[(buffer * kStepsV + step_v + y) * 64 + lane] = mine_v[y];
+    };
+
+    find(now.first);
+    fetch();
+    find(now.first + 1);
+    put(0);
+    for (int tile = now.first, buffer = 0; tile < now.end; ++tile, buffer ^= 1) {
+      fetch();
+      find(tile + 2);
+      // All waves' parts of this buffer are written, and the other buffer's are read.  (LDS alone is waited
+      // for: the loads above stay in flight.)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (wave_row < now.n * group) {
+#pragma unroll
+        for (int y = 0; y < kStepsK; ++y)
+          s.kf[y / L::kSteps][y % L::kSteps] = sh_k[(buffer * kStepsK + y) * 64 + lane];
+        f32x4 p[kRowTiles][L::kSub];
+        s.scores(p);
+#pragma unroll
+        for (int y = 0; y < kStepsV; ++y) {
+          const VecV v = sh_v[(buffer * kStepsV + y) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < L::kLoadWords; ++e) s.vf[y / L::kLoadsV][y % L::kLoadsV * L::kLoadWords + e] = v[e];
+        }
+        const int first = tile * L::kKeys;
+        if (first + L::kKeys - 1 > now.len) {
+          s.mask(p, first);
+          s.softmax(p);
+          s.products_edge(p, first, now.len, now.len + now.n);
+        } else {
+          s.softmax(p);
+          s.products(p);
+        }
+      }
+      put(buffer ^ 1);
+    }
+
+    const bool begins = now.first == 0, whole = begins && now.end == now.tiles;
+    const int slot = begins ? 1 : 0;
+    if (begins && !whole && threadIdx.x == 0)
+      plan.cut[wg] = CutSegment{range_of(at.end - now.end + now.tiles - 1, at.total, plan.log_ranges) - wg + 1,
+                                now.b, now.seg, now.n};
+    const bool mine_bad = __any(s.bad);
+    if (lane == 0) sh_bad[wave] = mine_bad;
+    __syncthreads();  // (also: all have read the buffers that the next piece writes)
+    int bad = 0;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) bad |= sh_bad[x];
+    s.bad = false;
+    int id = threadIdx.x & 63;  // (volatile: addresses are made here, not kept through the walk)
+    asm volatile("" : "+v"(id));
+    const int col = id & 15, g = id >> 4;
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
+      const int qrow = wave_row + 16 * t + col, i = qrow / group;
+      float sum = row_sum(s.l[t]), top = s.m[t];
+      if (bad) {
+        sum = __builtin_nanf("");
+        if (top == -INFINITY) top = 0.f;
+      }
+      if (i >= now.n) continue;
+      const long long row =
+          (static_cast<long long>(now.b) * (a.K + 1) + i) * a.q_heads + h * group + qrow - i * group;
+      const long long part_row = (2LL * wg + slot) * plan.rows + qrow - chunk * plan.rows;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < L::kOut; y += 4) {
+          const int d = L::kChunk * (4 * g + x) + y;
+          const f32x4 four = {s.o[t][y][x], s.o[t][y + 1][x], s.o[t][y + 2][x], s.o[t][y + 3][x]};
+          if (!whole)
+            *reinterpret_cast<f32x4*>(plan.part_o + part_row * kDim + d) = four;
+          else if (d < c.dim)
+            write_row<T>(a, c, row, d, four, top, sum);
+          __builtin_amdgcn_sched_barrier(0);  // (few copies of the outputs at a time)
+        }
+      if (!whole && g == 0) {
+        plan.part_m[part_row] = top;
+        plan.part_l[part_row] = sum;
+      }
+    }
+    if (left <= 0) return;
+    int nb = now.b, seg = now.seg + 1, nlen = now.len, nn = now.n;
+    if (seg == c.heads * now.chunks) {
+      seg = 0;
+      do {
+        const RoundRows x = round_rows(c, a.num_draft, a.kv_len, ++nb, a.K);
+        nlen = uniform(x.len);
+        nn = uniform(x.n);
+      } while (nn == 0);
+    }
+    now = make_piece<T, L::kKeys>(c, plan, group, nb, seg, nlen, nn, 0, left);
+  }
 }
 
 template <typename T, int kDim, bool kFast>
 void launch_attend_dim(const AttendArgs& a, const KvArgs& c, const AttendPlan& p) {
-  const dim3 grid(p.groups), block(kAttendThreads);
-  if (p.tile_rows == 1)
-    attend_split_kernel<T, kDim, kFast, 1, kDim == 256 ? 1 : 2><<<grid, block, 0, a.stream>>>(a, c, p);
-  else if constexpr (kDim < 256) {
-    if (p.tile_rows == 2)
-      attend_split_kernel<T, kDim, kFast, 2, kDim == 128 && sizeof(T) == 4 ? 1 : 2><<<grid, block, 0, a.stream>>>(a, c, p);
-    else if constexpr (kDim == 64 || sizeof(T) == 2)
-      attend_split_kernel<T, kDim, kFast, 4, 1><<<grid, block, 0, a.stream>>>(a, c, p);
+  const unsigned groups = 1u << (p.log_ranges - p.log_waves);
+  if (p.wide) {
+    constexpr unsigned kLds = 2 * 2 * Tile<T, kDim, kFast>::kKeys * kDim * sizeof(T);  // two tiles of K and V
+    if (p.rows == 64)
+      attend_wide_kernel<T, kDim, kFast, 1, 4><<<groups, 256, kLds, a.stream>>>(a, c, p);
+    else if constexpr (kDim == 128)
+      attend_wide_kernel<T, kDim, kFast, 1, 8><<<groups, 512, kLds, a.stream>>>(a, c, p);
+    else if constexpr (kDim == 64)
+      attend_wide_kernel<T, kDim, kFast, 2, 4><<<groups, 256, kLds, a.stream>>>(a, c, p);
+  } else if constexpr (kDim == 256) {
+    attend_split_kernel<T, kDim, kFast, 1, 1><<<groups, 64, 0, a.stream>>>(a, c, p);
+  } else {
+    const unsigned lds = 8 * p.rows * (kDim + 4) * sizeof(float);
+    if (p.rows == 16)
+      attend_split_kernel<T, kDim, kFast, 1, 4><<<groups, 256, lds, a.stream>>>(a, c, p);
+    else
+      attend_split_kernel<T, kDim, kFast, 2, 4><<<groups, 256, lds, a.stream>>>(a, c, p);
   }
-  launch_join<T, kDim>(a, c, p);
+  const int rows = p.rows < (a.K + 1) * (a.q_heads / c.heads) ? p.rows : (a.K + 1) * (a.q_heads / c.heads);
+  attend_join_kernel<T, kDim><<<dim3(groups, rows < 8 ? rows : 8), kJoinThreads, 0, a.stream>>>(a, c, p);
 }
 
 template <typename T>

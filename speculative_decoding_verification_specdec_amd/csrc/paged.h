@@ -112,7 +112,7 @@ hipError_t launch_rope(const RopeArgs& a, const KvArgs& c, int dtype);
 hipError_t launch_attend(const AttendArgs& a, const KvArgs& c, int dtype);
 hipError_t launch_kv_weights(const WeightArgs& a, const KvArgs& c, int dtype);
 hipError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, int dtype);
-size_t attend_workspace_bytes(int B, int K, int q_heads, int kv_heads, int dim);
+size_t attend_workspace_bytes(int K, int q_heads, int kv_heads, int dim);
 size_t evict_workspace_bytes(int B, int heads, long long capacity, int budget);
 
 }  // namespace specdec

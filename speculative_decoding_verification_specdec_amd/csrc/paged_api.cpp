@@ -189,7 +189,7 @@ size_t specdec_paged_attention_workspace_size(int32_t B, int32_t K, int32_t num_
   if (B <= 0 || K < 0 || K > SPECDEC_MAX_K || !heads_valid(num_q_heads, num_kv_heads) ||
       !rows_valid(B, K, num_q_heads) || !dim_valid(head_dim))
     return 0;
-  return specdec::attend_workspace_bytes(B, K, num_q_heads, num_kv_heads, head_dim);
+  return specdec::attend_workspace_bytes(K, num_q_heads, num_kv_heads, head_dim);
 }
 
 specdec_status specdec_paged_attention(const void* q, int64_t q_stride, int32_t B, int32_t K,
@@ -212,7 +212,7 @@ specdec_status specdec_paged_attention(const void* q, int64_t q_stride, int32_t 
       misaligned(kv_len, 4) || misaligned(workspace, 16) ||
       stride_misaligned(q_stride, B, K, cache->dtype))
     return SPECDEC_ERR_ALIGN;
-  if (workspace_bytes < specdec::attend_workspace_bytes(B, K, num_q_heads, kv_heads, dim))
+  if (workspace_bytes < specdec::attend_workspace_bytes(K, num_q_heads, kv_heads, dim))
     return SPECDEC_ERR_WORKSPACE;
   specdec::AttendArgs a{};
   a.q = q;

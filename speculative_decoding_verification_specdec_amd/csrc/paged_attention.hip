@@ -6,11 +6,11 @@
 //
 // Bound: the cache's bytes.  A round has few rows (tokens x heads of a group), 4 rows flops a byte of the
 // cache, which the matrix cores do in a tenth of the time that the bytes take; so the work is cut by
-// bytes.  Sequences differ in length and one long one must not decide the time: the units of 128 slots of
-// all (sequence, kv head, row chunk) segments are laid end to end and cut into equal contiguous ranges,
-// one a workgroup.  A segment that lies in one range is written at once; the others leave one part a
-// range (at most two a workgroup), which the join adds up.  A range ends in the first part of at most one
-// cut segment, which it notes, so the join has as many workgroups to look at as there are ranges.
+// bytes.  Sequences differ in length and one long one must not decide the time: the 32-slot tiles of all
+// (sequence, kv head, chunk of rows) segments are laid end to end and cut into equal contiguous ranges, one a
+// wave.  A segment that lies in one range is written at once; the others leave one part a range (at most
+// two a wave), which the join adds up.  A range ends in the first part of at most one cut segment, which
+// it notes, so the join has as many segments to look at as there are ranges.
 #include <hip/hip_runtime.h>
 
 #include "attend_dev.h"
@@ -18,18 +18,23 @@
 namespace specdec {
 namespace {
 
-// The row tiles and waves for the rows of a group: 16-row tiles a wave as needed up to what the
-// registers hold (4; 1 for the widest heads), then more waves by rows, then chunks.
-AttendPlan make_plan(int B, int K, int q_heads, int kv_heads, int dim, bool f32) {
+// Up to 32 rows (16 of the widest heads, as their registers allow) every wave takes all rows of its own range:
+// 1024 ranges, one wave a SIMD, four of them a workgroup where the LDS holds their parts.  More rows are shared
+// out to the waves of a workgroup, 64 or 128 a chunk, with a range for each workgroup that is resident: 512, or
+// 256 where eight waves or the LDS allow one a CU.
+AttendPlan make_plan(int K, int q_heads, int kv_heads, int dim) {
   AttendPlan p{};
   const int rows = (K + 1) * (q_heads / kv_heads);
   p.dim = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  p.tile_rows = rows <= 16 || p.dim == 256 ? 1 : rows <= 32 || (f32 && p.dim == 128) ? 2 : 4;
-  const int wave_rows = 16 * p.tile_rows;
-  p.row_waves = rows <= wave_rows ? 1 : rows <= 2 * wave_rows ? 2 : 4;
-  p.rows = wave_rows * p.row_waves;
-  p.chunks = (rows + p.rows - 1) / p.rows;
-  p.groups = kAttendGroups;
+  p.wide = rows > (p.dim == 256 ? 16 : 32);
+  if (p.wide) {
+    p.rows = rows <= 64 || p.dim == 256 ? 64 : 128;
+    p.log_ranges = p.dim == 256 || (p.dim == 128 && p.rows == 128) ? 8 : 9;
+  } else {
+    p.rows = rows <= 16 ? 16 : 32;
+    p.log_ranges = 10;
+    p.log_waves = p.dim == 256 ? 0 : 2;
+  }
   return p;
 }
 
@@ -37,18 +42,18 @@ size_t align16(size_t x) { return (x + 15) & ~size_t{15}; }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int B, int K, int q_heads, int kv_heads, int dim) {
-  const AttendPlan p = make_plan(B, K, q_heads, kv_heads, dim, false);  // (f32 has no more rows)
-  const size_t part_rows = 2 * static_cast<size_t>(p.groups) * p.rows;
-  return p.groups * sizeof(CutSegment) + part_rows * p.dim * 4 + 2 * align16(part_rows * 4);
+size_t attend_workspace_bytes(int K, int q_heads, int kv_heads, int dim) {
+  const AttendPlan p = make_plan(K, q_heads, kv_heads, dim);
+  const size_t groups = size_t{1} << (p.log_ranges - p.log_waves), part_rows = 2 * groups * p.rows;
+  return groups * sizeof(CutSegment) + part_rows * p.dim * 4 + 2 * align16(part_rows * 4);
 }
 
 hipError_t launch_attend(const AttendArgs& a, const KvArgs& c, int dtype) {
-  AttendPlan p = make_plan(a.B, a.K, a.q_heads, c.heads, c.dim, dtype == 0);
-  const size_t part_rows = 2 * static_cast<size_t>(p.groups) * p.rows;
+  AttendPlan p = make_plan(a.K, a.q_heads, c.heads, c.dim);
+  const size_t groups = size_t{1} << (p.log_ranges - p.log_waves), part_rows = 2 * groups * p.rows;
   char* ws = static_cast<char*>(a.workspace);
   p.cut = reinterpret_cast<CutSegment*>(ws);
-  ws += p.groups * sizeof(CutSegment);
+  ws += groups * sizeof(CutSegment);
   p.part_o = reinterpret_cast<float*>(ws);
   ws += part_rows * p.dim * 4;
   p.part_m = reinterpret_cast<float*>(ws);

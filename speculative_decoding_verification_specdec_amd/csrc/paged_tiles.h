@@ -62,14 +62,25 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
   return __builtin_bit_cast(unsigned, p);
 }
 
+// Global memory by its own pointer type, so that a base known to be wave-uniform stays scalar.
+typedef const __attribute__((address_space(1))) char* GlobalBytes;
+
+// A lane's 32-bit offset as it is where it is used: hoisted out of a loop it would be widened to 64 bits
+// there, and the load could not take it beside a scalar base.
+__device__ __forceinline__ unsigned lane_offset(unsigned x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // A load; kStream: of bytes that nothing reads again (a stream of such loads reaches 7.1-7.3 TB/s on
 // MI355X, one of plain loads 6.0-6.4: 4 GiB, any grid from 256 to 16384 workgroups).
 template <typename V, bool kStream>
-__device__ __forceinline__ V load(const void* p) {
+__device__ __forceinline__ V load(GlobalBytes p) {
+  typedef const __attribute__((address_space(1))) V* Pointer;
   if constexpr (kStream)
-    return __builtin_nontemporal_load(static_cast<const V*>(p));
+    return __builtin_nontemporal_load((Pointer)p);
   else
-    return *static_cast<const V*>(p);
+    return *(Pointer)p;
 }
 
 // kDim: head_dim rounded up to 64, 128 or 256; kFull: equal to it; else the rest of a
@@ -89,37 +100,45 @@ struct Tile {
   // A lane's part of a row of K or Q: kVec elements from 4 kVec s + kVec g on, for every step s.  The row
   // lies `off` elements from `base`; a wave-uniform base keeps the 64-bit part of the address scalar.
   template <bool kStream>
-  static __device__ __forceinline__ void load_row(u32x4 (&f)[kSteps], const T* base, unsigned off, int g,
+  static __device__ __forceinline__ void load_row(u32x4 (&f)[kSteps], GlobalBytes base, unsigned off, int g,
                                                   int dim) {
-    const unsigned at = (off + kVec * g) * static_cast<unsigned>(sizeof(T));
+    const unsigned at = lane_offset((off + kVec * g) * static_cast<unsigned>(sizeof(T)));
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       f[s] = u32x4{0, 0, 0, 0};
       if (kFull || 4 * kVec * s + kVec * g < dim)
-        f[s] = load<u32x4, kStream>(reinterpret_cast<const char*>(base) + at + 64 * s);
+        f[s] = load<u32x4, kStream>(base + at + 64 * s);
     }
   }
 
-  // kChunk elements of a row of V from kChunk * (lane % 16) on.
+  // One of those loads.
   template <bool kStream>
-  static __device__ __forceinline__ void load_v(unsigned (&f)[kWords], const T* base, unsigned off, int col,
+  static __device__ __forceinline__ u32x4 load_step(GlobalBytes base, unsigned off, int s, int g, int dim) {
+    const unsigned at = lane_offset((off + 4 * kVec * s + kVec * g) * static_cast<unsigned>(sizeof(T)));
+    u32x4 x = {0, 0, 0, 0};
+    if (kFull || 4 * kVec * s + kVec * g < dim) x = load<u32x4, kStream>(base + at);
+    return x;
+  }
+
+  // A lane's kChunk elements of a row of V, from kChunk * (lane % 16) on: load z of kLoadsV.
+  static constexpr int kLoadsV = kWords < 4 ? 1 : kWords / 4;
+  static constexpr int kLoadWords = kWords / kLoadsV;
+  typedef unsigned LoadV __attribute__((ext_vector_type(kLoadWords)));
+  template <bool kStream>
+  static __device__ __forceinline__ LoadV load_v_step(GlobalBytes base, unsigned off, int z, int col, int dim) {
+    const unsigned at = lane_offset((off + kChunk * col) * static_cast<unsigned>(sizeof(T)) + 16 * z);
+    LoadV x = {};
+    if (kFull || kChunk * col + z * kVec < dim) x = load<LoadV, kStream>(base + at);
+    return x;
+  }
+  template <bool kStream>
+  static __device__ __forceinline__ void load_v(unsigned (&f)[kWords], GlobalBytes base, unsigned off, int col,
                                                 int dim) {
-    const unsigned at = (off + kChunk * col) * static_cast<unsigned>(sizeof(T));
-    const char* p = reinterpret_cast<const char*>(base);
-    if constexpr (kWords == 2) {
-      u32x2 x = {0, 0};
-      if (kFull || kChunk * col < dim) x = load<u32x2, kStream>(p + at);
-      f[0] = x[0];
-      f[1] = x[1];
-    } else {
 #pragma unroll
-      for (int w = 0; w < kWords; w += 4) {
-        u32x4 x = {0, 0, 0, 0};
-        if (kFull || kChunk * col + w * 4 / static_cast<int>(sizeof(T)) < dim)
-          x = load<u32x4, kStream>(p + at + 4 * w);
+    for (int z = 0; z < kLoadsV; ++z) {
+      const LoadV x = load_v_step<kStream>(base, off, z, col, dim);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[w + e] = x[e];
-      }
+      for (int e = 0; e < kLoadWords; ++e) f[z * kLoadWords + e] = x[e];
     }
   }
 
