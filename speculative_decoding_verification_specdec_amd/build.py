@@ -15,12 +15,13 @@ PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / "kernels.hip", PKG / "csrc" / "fused.hip", PKG / "csrc" / "small.hip", PKG / "csrc" / "ngram.hip",
            PKG / "csrc" / "commit.hip", PKG / "csrc" / "noalloc.hip", PKG / "csrc" / "quad.hip",
-           PKG / "csrc" / "telemetry.hip", PKG / "csrc" / "rope.hip", PKG / "csrc" / "paged_attention.hip",
+           PKG / "csrc" / "telemetry.hip", PKG / "csrc" / "rope.hip",
            PKG / "csrc" / "attend_bf16.hip", PKG / "csrc" / "attend_f16.hip", PKG / "csrc" / "attend_f32.hip",
            PKG / "csrc" / "kv_weights.hip", PKG / "csrc" / "kv_evict.hip",
-           PKG / "csrc" / "api.cpp", PKG / "csrc" / "telemetry.cpp", PKG / "csrc" / "paged_api.cpp"]
+           PKG / "csrc" / "api.cpp", PKG / "csrc" / "telemetry.cpp", PKG / "csrc" / "paged_api.cpp",
+           PKG / "csrc" / "paged_attention.cpp"]
 HEADERS = [PKG / "csrc" / "kernels.h", PKG / "csrc" / "paged.h",
-           PKG / "csrc" / "paged_tiles.h", PKG / "csrc" / "attend_dev.h", PKG / "csrc" / "verify_dev.h", PKG / "csrc" / "wave_ops.h", ROOT / "include" / "specdec.h"]
+           PKG / "csrc" / "paged_tiles.h", PKG / "csrc" / "attend_dev.h", PKG / "csrc" / "attend_plan.h", PKG / "csrc" / "verify_dev.h", PKG / "csrc" / "wave_ops.h", ROOT / "include" / "specdec.h"]
 OUTPUT = PKG / "libspecdec.so"
 ARCH = os.environ.get("SPECDEC_OFFLOAD_ARCH", "gfx950")
 

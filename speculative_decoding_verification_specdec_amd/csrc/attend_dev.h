@@ -1,37 +1,16 @@
-// The attention kernel over the paged cache (see paged_attention.hip for the split and the join),
+// The attention kernels over the paged cache (paged_attention.cpp makes the plan they follow),
 // instantiated for one element type in each of attend_bf16.hip, attend_f16.hip and attend_f32.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
+#include "attend_plan.h"
 #include "paged_tiles.h"
 #include "wave_ops.h"
 
 namespace specdec {
 
 constexpr int kJoinThreads = 256;
-
-// A segment that lies in the ranges of several workgroups: parts of workgroups w .. w + parts - 1 (parts 0:
-// none); n: its sequence's new tokens.
-struct alignas(32) CutSegment {
-  int parts, b, seg, n;
-};
-
-// How a call is cut.  A segment is one (sequence, kv head, chunk of its query rows); its tiles, and those of all
-// segments one after the other, are dealt out evenly to 1 << log_ranges waves in contiguous ranges.
-struct AttendPlan {
-  int log_ranges;
-  int log_waves;        // log2(ranges a workgroup), neighbouring ones
-  int wide;             // the kernel for many rows: one range a workgroup
-  int rows;             // rows of a chunk: 16 a row tile
-  int dim;              // kDim of the kernel
-  int page_shift;       // log2(page_size), or -1
-  float scale_log2;     // scale * log2(e)
-  CutSegment* cut;      // [workgroups] the cut segment whose first part a workgroup holds
-  float* part_o;        // [2 workgroups][rows][dim] unnormalised outputs: of the segment that comes from the
-  float* part_m;        // [2 workgroups][rows]      workgroup before (0) and of the one that begins here (1);
-  float* part_l;        // [2 workgroups][rows]      their bases (of scores * log2(e)) and sums
-};
 
 // Row chunks of a sequence with n new tokens; tiles of its slots; tiles of all its segments (none if it
 // is invalid).
@@ -1116,9 +1095,5 @@ void launch_attend_type(const AttendArgs& a, const KvArgs& c, const AttendPlan& 
   else
     fast ? launch_attend_dim<T, 256, true>(a, c, p) : launch_attend_dim<T, 256, false>(a, c, p);
 }
-
-void launch_attend_bf16(const AttendArgs& a, const KvArgs& c, const AttendPlan& p);
-void launch_attend_f16(const AttendArgs& a, const KvArgs& c, const AttendPlan& p);
-void launch_attend_f32(const AttendArgs& a, const KvArgs& c, const AttendPlan& p);
 
 }  // namespace specdec

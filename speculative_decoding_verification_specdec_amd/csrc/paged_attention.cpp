@@ -13,7 +13,7 @@
 // it notes, so the join has as many segments to look at as there are ranges.
 #include <hip/hip_runtime.h>
 
-#include "attend_dev.h"
+#include "attend_plan.h"
 
 namespace specdec {
 namespace {
@@ -61,7 +61,7 @@ hipError_t launch_attend(const AttendArgs& a, const KvArgs& c, int dtype) {
   p.part_l = reinterpret_cast<float*>(ws);
   p.page_shift = -1;
   if ((c.page_size & (c.page_size - 1)) == 0) p.page_shift = __builtin_ctz(c.page_size);
-  p.scale_log2 = a.scale * kLog2e;
+  p.scale_log2 = a.scale * 1.44269504088896340736f;
   if (dtype == 0)
     launch_attend_f32(a, c, p);
   else if (dtype == 1)
