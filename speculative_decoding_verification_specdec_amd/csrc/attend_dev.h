@@ -38,7 +38,7 @@ __device__ __forceinline__ int range_of(long long tile, long long total, int log
   return static_cast<int>(q);
 }
 
-// Maximum and sum over the four lanes 16 apart that share a row: each step swaps halves of two copies.
+// Maximum over the four lanes 16 apart that share a row (like row_sum).
 __device__ __forceinline__ float row_max(float x) {
   const unsigned u = __float_as_uint(x);
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
@@ -46,28 +46,6 @@ __device__ __forceinline__ float row_max(float x) {
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float row_sum(float x) {
-  const unsigned u = __float_as_uint(x);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const unsigned v = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
-__device__ __forceinline__ long long shfl64(long long x, int src) {
-  const int lo = __shfl(static_cast<int>(x), src, 64);
-  const int hi = __shfl(static_cast<int>(x >> 32), src, 64);
-  return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo);
-}
-
-__device__ __forceinline__ long long read_lane64(long long x, int src) {
-  const int lo = __builtin_amdgcn_readlane(static_cast<int>(x), src);
-  const int hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), src);
-  return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo);
-}
-
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
 // Where a tile's rows lie.  kPaged16: pages are whole 16-slot groups, so each group has one page and a
 // wave-uniform address, and lanes add 32-bit offsets that stay the same for the whole walk; otherwise a
 // lane looks up one slot and the others get its row by shuffles.
@@ -75,22 +53,6 @@ template <bool kPaged16, int kSub>
 struct TileRows {
   long long at[kPaged16 ? kSub : 1];
 };
-
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
-// A wave-uniform pointer as it is, in scalar registers: without this the compiler adds the lanes' offsets
-// to its loop-invariant part and keeps a 64-bit vector address for each row.
-__device__ __forceinline__ GlobalBytes scalar_base(const void* p) {
-  unsigned long long bits = reinterpret_cast<uintptr_t>(p);
-  asm("" : "+s"(bits));
-  return (GlobalBytes)bits;
-}
-
-// A page-table entry at a wave-uniform place, by a scalar load.
-__device__ __forceinline__ int table_at(const int32_t* table, long long i) {
-  typedef const __attribute__((address_space(4))) int32_t* Scalar;
-  return *(Scalar)(reinterpret_cast<uintptr_t>(table + i));
-}
 
 // One piece of a wave's range: tiles [first, end) of a segment (b, seg = kv head * chunks + chunk) of `tiles`;
 // none: end 0.
