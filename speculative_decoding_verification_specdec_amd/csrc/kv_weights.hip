@@ -7,7 +7,9 @@
 //
 // Bound: the bytes of K and of the weights, which are read and written; each byte of K once, streamed from
 // memory to registers.  The query rows, which all slots of a segment (one sequence and kv head) share, lie in LDS
-// operand by operand.  The tiles of all segments, laid end to end and weighed by what they cost, are cut into
+// operand by operand.  (Plain loads: streaming ones, which are faster where nothing is written, took 543 us for
+// 64 x 16380 slots of 8 heads where plain ones take 481, 391 of them without the weights' stores; holding stores back
+// in LDS for 4-16 tiles changed that by 1%.)  The tiles of all segments, laid end to end and weighed by what they cost, are cut into
 // equal ranges, one a workgroup, whose four waves take the range's tiles in turn.
 #include <hip/hip_runtime.h>
 
@@ -95,7 +97,7 @@ struct WeightWave {
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub) {
         const bool good = static_cast<unsigned>(page[sub]) < static_cast<unsigned>(c.num_pages);
-        L::template load_row<true>(
+        L::template load_row<false>(
             k.f[sub], scalar_base(kpool + ((good ? page[sub] : 0) * c.page_stride + off[sub] * c.slot_stride)),
             static_cast<unsigned>(col) * static_cast<unsigned>(c.slot_stride), g, c.dim);
         if (mine >> 4 == sub) k.record = good && used ? record_at(c, page[sub], off[sub] + col, head) : -1;
@@ -108,7 +110,7 @@ struct WeightWave {
       k.record = good && used ? record_at(c, page, off, head) : -1;
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub)
-        L::template load_row<true>(k.f[sub], (GlobalBytes)(kpool + shfl64(row, 16 * sub + col)), 0u, g, c.dim);
+        L::template load_row<false>(k.f[sub], (GlobalBytes)(kpool + shfl64(row, 16 * sub + col)), 0u, g, c.dim);
     }
   }
 
