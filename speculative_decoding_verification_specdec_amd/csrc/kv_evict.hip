@@ -1,15 +1,17 @@
 // gfx950 kernels of the eviction by accumulated attention weight.
 //
 // Of a (sequence, kv head)'s L slots the `budget` ones with the largest keys stay; a key is the order of the weight
-// as an unsigned number, with protected positions above all.  One workgroup per sequence and head reads the records
-// once, finds the budget-th largest key by a radix search (11, 11 and 10 bits) over keys that it keeps in LDS, or in
-// the workspace where the cache can hold more slots than fit, and then walks over them in order.  A slot's rank is
-// what decides:  with G(s) and T(s) the slots before s that lie above the threshold key and at it, and `left` the
-// number at it that stay,
+// as an unsigned number, with protected positions above all.  A radix search (11, 11 and 10 bits) finds the budget-th
+// largest key; then the slots are walked over in order.  A slot's rank is what decides:  with G(s) and T(s) the slots
+// before s that lie above the threshold key and at it, and `left` the number at it that stay,
 //   kept before s = G(s) + min(T(s), left),
 // which is the place among the holes of an evicted slot s < budget (s - kept before s) and, counted from the end, of
 // a kept slot s >= budget among the movers.  There are as many of one as of the other, and mover i is copied over
 // hole i.  Sources lie at or above `budget` and destinations below it, so the copies are independent of each other.
+//
+// Few slots: one workgroup per sequence and head reads the records once and does everything, keys and positions in
+// registers.  Many: a workgroup has 4096 slots of a pair, and each pass is a launch, as the next needs all
+// workgroups' counts; the keys lie in the workspace.
 //
 // Bound: for a full cache that gives up a round's slots the latency of one workgroup's passes (the records are 8
 // bytes a slot); for a deep cut the rows that move.
@@ -23,33 +25,49 @@ namespace specdec {
 namespace {
 
 constexpr int kGroup = 256;        // slots a wave takes at once, four a lane
-constexpr int kLdsSlots = 8192;    // keys and positions in LDS up to so many: 64 KiB, two workgroups a CU
 constexpr int kBins = 2048;
+constexpr int kFewWaves = 8, kFewHold = 4;       // groups that a wave holds: up to 8192 slots
+constexpr int kFewSlots = kFewWaves * kFewHold * kGroup;
+constexpr int kPartWaves = 4, kPartHold = 4;     // of a part
+constexpr int kPartSlots = kPartWaves * kPartHold * kGroup;
 constexpr int kMoveWaves = 4;
 constexpr int kMoveBatch = 16;     // rows that a wave moves at once
 // The select kernel's workgroup moves the rows itself where there cannot be more than these: a second launch would
 // take longer.
 constexpr int kOwnMoves = 256;
 
-// Workspace: per (sequence, head) the number of moves, the movers and the holes; where LDS is too small also keys and
-// positions.
+// What the passes over many slots leave of a (sequence, head).
+struct EvictState {
+  unsigned threshold;
+  int left;
+};
+struct PartRecord {
+  int newest, bad;    // of a part's slots: the largest position, a page outside the pool
+  int above, ties;    // and those above the threshold and at it
+};
+
+// Workspace: per (sequence, head) the number of moves, the movers and the holes; for caches of many slots also what
+// the passes hand on.
 struct EvictLists {
   int32_t* count;
-  int32_t* from;     // the movers, at the end of `most` places
-  int32_t* to;       // the holes, from the first place on
-  long long most;    // entries per (sequence, head)
-  unsigned* keys;    // [2][slots] per (sequence, head)
-  long long slots;   // capacity rounded up to whole groups
-  int own_moves;     // the select kernel moves the rows and writes new_len
-  unsigned magic;    // 2^32 / (16-byte vectors of a row of k and v) rounded up
+  int32_t* from;       // the movers, at the end of `most` places
+  int32_t* to;         // the holes, from the first place on
+  long long most;      // entries per (sequence, head)
+  unsigned* keys;      // [slots] per (sequence, head)
+  unsigned* positions;
+  unsigned* hist;      // [3][kBins]
+  EvictState* state;   // [3], after each pass
+  PartRecord* part;    // [parts]
+  long long slots;     // capacity rounded up to whole parts
+  int parts;
+  int own_moves;       // the select kernel moves the rows and writes new_len
+  unsigned magic;      // 2^32 / (16-byte vectors of a row of k and v) rounded up
 };
 
 long long most_moves(long long capacity, int budget) {
   return capacity <= budget ? 0 : capacity - budget < budget ? capacity - budget : budget;
 }
-long long whole_groups(long long capacity) { return (capacity + kGroup - 1) / kGroup * kGroup; }
-
-size_t align16(size_t x) { return (x + 15) & ~size_t{15}; }
+long long part_count(long long capacity) { return (capacity + kPartSlots - 1) / kPartSlots; }
 
 // Unsigned order of a weight: NaN 0, then ascending; -0 and +0 alike.
 __device__ __forceinline__ unsigned weight_order(float w) {
@@ -66,19 +84,6 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
   return v;
-}
-
-// Counts a digit; a wave whose lanes all have the same one (zero weights, protected slots) adds them at once.
-__device__ __forceinline__ void count_digit(unsigned* hist, unsigned digit, bool active, int lane) {
-  const unsigned long long who = __ballot(active);
-  if (who == 0) return;
-  const int leader = __builtin_ctzll(who);
-  const unsigned first = __builtin_amdgcn_readlane(digit, leader);
-  if (__ballot(active && digit == first) == who) {
-    if (lane == leader) atomicAdd(&hist[first], static_cast<unsigned>(__popcll(who)));
-  } else if (active) {
-    atomicAdd(&hist[digit], 1u);
-  }
 }
 
 // Copies movers [first, first + count) of `total` over their holes; count <= kMoveBatch.  kFlight: 16-byte loads of a
@@ -108,7 +113,8 @@ __device__ __forceinline__ void move_rows(const KvArgs& c, const EvictLists& lis
     for (int y = 0; y < kFlight; ++y) {
       const int x = min(x0 + 64 * y + lane, all - 1);
       const int m = static_cast<int>(__umulhi(static_cast<unsigned>(x), lists.magic)), z = x - m * row;
-      const uintptr_t pool = reinterpret_cast<uintptr_t>(z < vectors ? c.k : c.v) + 16 * (z < vectors ? z : z - vectors);
+      const char* part = z < vectors ? c.k : c.v;
+      const uintptr_t pool = reinterpret_cast<uintptr_t>(part) + 16 * (z < vectors ? z : z - vectors);
       to[y] = (Rows)(pool + shfl64(dst, m));
       data[y] = *(Rows)(pool + shfl64(src, m));
     }
@@ -118,26 +124,189 @@ __device__ __forceinline__ void move_rows(const KvArgs& c, const EvictLists& lis
   }
 }
 
-// Threads of a workgroup.  Few slots: a pair has little work and there are many of them, two or three a CU.
-constexpr int select_threads(bool lds) { return lds ? 512 : 1024; }
+// A group's part in a lane: the records of four slots from `slot` on, as they are.  kQuad: four slots from a multiple
+// of four on lie in one page.
+template <bool kQuad>
+struct RecordAt {
+  int page[kQuad ? 1 : 4], off[kQuad ? 1 : 4];
 
-// kLds: keys and positions of all slots lie in LDS.  kQuad: four slots from a multiple of four on lie in one page.
-template <bool kLds, bool kQuad>
-__global__ __launch_bounds__(select_threads(kLds), 4) void evict_select_kernel(EvictArgs a, KvArgs c,
-                                                                               EvictLists lists, int esize) {
-  constexpr int kThreads = select_threads(kLds), kWaves = kThreads / 64, kMine = kBins / kThreads;
-  extern __shared__ u32x4 sh_slots[];  // [2][lists.slots / 4]
+  __device__ __forceinline__ void find(const KvArgs& c, const int32_t* table, int slot, int L) {
+    const int s0 = min(slot, (L - 1) & ~3);  // (past the last slot: the last ones again)
+#pragma unroll
+    for (int j = 0; j < (kQuad ? 1 : 4); ++j) {
+      const int s = min(s0 + j, L - 1), idx = s / c.page_size;
+      off[j] = s - idx * c.page_size;
+      page[j] = table[idx];
+    }
+  }
+  __device__ __forceinline__ void load(const KvArgs& c, int h, u32x4& weight, u32x4& pos, bool& bad) const {
+    typedef unsigned Words __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int j = 0; j < (kQuad ? 1 : 4); ++j) {
+      const bool good = static_cast<unsigned>(page[j]) < static_cast<unsigned>(c.num_pages);
+      bad = bad || !good;
+      const long long r = record_at(c, good ? page[j] : 0, off[j], h);
+      if constexpr (kQuad) {
+        pos = *reinterpret_cast<const Words*>(c.position + r);
+        weight = *reinterpret_cast<const Words*>(c.weight + r);
+      } else {
+        pos[j] = static_cast<unsigned>(c.position[r]);
+        weight[j] = __float_as_uint(c.weight[r]);
+      }
+    }
+  }
+};
+
+// Weights to keys; the largest position of slots before L.
+__device__ __forceinline__ u32x4 keys_of(u32x4 weight, const u32x4& pos, int slot, int L, int keep_first, int& newest) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int p = static_cast<int>(pos[j]);
+    if (slot + j < L) newest = max(newest, p);
+    weight[j] = p < keep_first ? 0xffffffffu : weight_order(__uint_as_float(weight[j]));
+  }
+  return weight;
+}
+__device__ __forceinline__ void protect(u32x4& key, const u32x4& pos, long long recent) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (static_cast<int>(pos[j]) > recent) key[j] = 0xffffffffu;
+}
+
+struct Digit {
+  int shift;
+  unsigned bits, above, prefix;  // (key & above) == prefix: the digits before are the threshold's
+};
+// Counts a group's digits.  Where all are the same (zero weights, protected slots) they are added at once: additions
+// to one address go one at a time.
+__device__ __forceinline__ void count_keys(unsigned* hist, const u32x4& key, int slot, int L, const Digit& d,
+                                           int lane) {
+  bool in[4], any = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    in[j] = slot + j < L && (key[j] & d.above) == d.prefix;
+    any = any || in[j];
+  }
+  if (!__any(any)) return;
+  const unsigned first = uniform(key[0]) >> d.shift & d.bits;
+  bool same = true;
+  unsigned digit[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    digit[j] = key[j] >> d.shift & d.bits;
+    same = same && in[j] && digit[j] == first;
+  }
+  if (__all(same)) {
+    if (lane == 0) atomicAdd(&hist[first], 256u);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (in[j]) atomicAdd(&hist[digit[j]], 1u);
+}
+__device__ __forceinline__ void count_order(const u32x4& key, int slot, int L, unsigned threshold, int& above,
+                                            int& ties) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    above += slot + j < L && key[j] > threshold;
+    ties += slot + j < L && key[j] == threshold;
+  }
+}
+
+// Lists a group's movers and holes; `above` and `ties` are those before the group, then those before the next.
+__device__ __forceinline__ void list_moves(const EvictLists& lists, long long bh, const u32x4& key, int slot, int L,
+                                           unsigned threshold, int left, int budget, int& above, int& ties,
+                                           int* stay) {
+  int mine = 0;  // above the threshold and (from bit 16 on) at it
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    mine += slot + j >= L ? 0 : key[j] > threshold ? 1 : key[j] == threshold ? 0x10000 : 0;
+  const int upto = wave_scan(mine);
+  int g = above + ((upto - mine) & 0xffff), t = ties + ((upto - mine) >> 16);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = slot + j < L, tie = key[j] == threshold;
+    const bool kept = key[j] > threshold || (tie && t < left);
+    const int before = g + min(t, left);
+    if (in && kept && slot + j >= budget) lists.from[bh * lists.most + lists.most - budget + before] = slot + j;
+    if (in && !kept && slot + j < budget) lists.to[bh * lists.most + slot + j - before] = slot + j;
+    if (slot + j == budget - 1) *stay = before + kept;
+    g += key[j] > threshold;
+    t += tie;
+  }
+  const int all = __builtin_amdgcn_readlane(upto, 63);
+  above += all & 0xffff;
+  ties += all >> 16;
+}
+
+// The digit at which the counts, from the highest digit down, reach `left`, which becomes what is left of it.  A thread
+// has kMine of the kBins counts, the highest first; exactly one digit of all fits.  The workgroup's threads come
+// together twice.
+template <int kWaves, int kMine>
+__device__ __forceinline__ unsigned find_digit(const int (&n)[kMine], int& left, int (&sh_sum)[kWaves],
+                                               int (&sh_found)[2], int tid, int lane, int wave) {
+  int mine = 0;
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) mine += n[x];
+  const int upto = wave_scan(mine);
+  if (lane == 63) sh_sum[wave] = upto;
+  __syncthreads();
+  int before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) before += w < wave ? sh_sum[w] : 0;
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) {
+    if (before < left && left <= before + n[x]) {
+      sh_found[0] = kBins - 1 - kMine * tid - x;
+      sh_found[1] = left - before;
+    }
+    before += n[x];
+  }
+  __syncthreads();
+  left = sh_found[1];
+  return static_cast<unsigned>(sh_found[0]);
+}
+
+__device__ __forceinline__ Digit digit_of(int pass, unsigned threshold) {
+  return Digit{pass == 0 ? 21 : pass == 1 ? 10 : 0, pass == 2 ? 1023u : 2047u,
+               pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10), threshold};
+}
+
+// The groups [g0, g0 + kHold) that exist (below g1) of a wave: records to registers, four groups on their way at once.
+template <int kHold, bool kQuad>
+__device__ __forceinline__ void load_records(const KvArgs& c, const int32_t* table, int h, int g0, int g1, int L,
+                                             int keep_first, int lane, u32x4 (&key)[kHold], u32x4 (&pos)[kHold],
+                                             int& newest, bool& bad) {
+  RecordAt<kQuad> at[kHold];
+  if (g0 >= g1) return;
+#pragma unroll
+  for (int x = 0; x < kHold; ++x) at[x].find(c, table, min(g0 + x, g1 - 1) * kGroup + 4 * lane, L);
+#pragma unroll
+  for (int x = 0; x < kHold; ++x) at[x].load(c, h, key[x], pos[x], bad);
+#pragma unroll
+  for (int x = 0; x < kHold; ++x)
+    if (g0 + x < g1) key[x] = keys_of(key[x], pos[x], (g0 + x) * kGroup + 4 * lane, L, keep_first, newest);
+}
+
+__device__ __forceinline__ int wave_max_i(int x) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) x = max(x, __shfl_xor(x, off, 64));
+  return x;
+}
+
+template <bool kQuad>
+__global__ __launch_bounds__(64 * kFewWaves, 4) void evict_select_kernel(EvictArgs a, KvArgs c, EvictLists lists,
+                                                                         int esize) {
+  constexpr int kThreads = 64 * kFewWaves, kMine = kBins / kThreads;
   __shared__ unsigned sh_hist[kBins];
-  __shared__ int sh_wave[2][kWaves];
-  __shared__ int sh_digit, sh_left;
+  __shared__ int sh_wave[2][kFewWaves];
+  __shared__ int sh_found[2], sh_stay;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
   const long long pairs = static_cast<long long>(a.B) * c.heads;
-  typedef int Int4 __attribute__((ext_vector_type(4), aligned(4)));
-  typedef float Float4 __attribute__((ext_vector_type(4), aligned(4)));
   for (long long bh = blockIdx.x; bh < pairs; bh += gridDim.x) {
-    const int b = static_cast<int>(bh / c.heads), h = static_cast<int>(bh - (bh / c.heads) * c.heads);
-    const int L = a.kv_len[b];
+    const int b = static_cast<int>(bh / c.heads), h = static_cast<int>(bh - static_cast<long long>(b) * c.heads);
+    const int L = uniform(a.kv_len[b]);
     const bool wrong = L < 0 || L > cap;
     __syncthreads();  // (LDS of the pair before)
     if (wrong || L <= a.budget) {
@@ -145,70 +314,15 @@ __global__ __launch_bounds__(select_threads(kLds), 4) void evict_select_kernel(E
       if (tid == 0 && lists.own_moves && h == 0 && a.new_len) a.new_len[b] = wrong ? -1 : L;
       continue;
     }
-    u32x4* keys;
-    if constexpr (kLds)
-      keys = sh_slots;
-    else
-      keys = reinterpret_cast<u32x4*>(lists.keys + 2 * bh * lists.slots);
-    u32x4* positions = keys + lists.slots / 4;
-    // Every wave has a run of groups; all passes take the same slots in the same lanes.
+    // Every wave has a run of groups; their keys stay in registers.
     const int groups = (L + kGroup - 1) / kGroup;
-    const int g0 = static_cast<int>(static_cast<long long>(groups) * wave / kWaves);
-    const int g1 = static_cast<int>(static_cast<long long>(groups) * (wave + 1) / kWaves);
+    const int g0 = groups * wave / kFewWaves, g1 = groups * (wave + 1) / kFewWaves;
     const int32_t* table = c.table + static_cast<long long>(b) * c.max_pages;
-
-    // Records to keys and positions, four groups on their way at once.
+    u32x4 key[kFewHold] = {}, pos[kFewHold] = {};
     int newest = -0x7fffffff - 1;
     bool bad = false;
-    for (int gi = g0; gi < g1; gi += 4) {
-      int page[4][kQuad ? 1 : 4];
-      long long at[4][kQuad ? 1 : 4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int j = 0; j < (kQuad ? 1 : 4); ++j) {
-          const int s = min(min(gi + u, g1 - 1) * kGroup + 4 * lane, (L - 1) & ~3) + j;
-          const int idx = s / c.page_size;
-          at[u][j] = s - idx * c.page_size;
-          page[u][j] = table[min(s, L - 1) / c.page_size];
-        }
-      u32x4 order[4], pos[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (kQuad) {
-          const bool good = static_cast<unsigned>(page[u][0]) < static_cast<unsigned>(c.num_pages);
-          bad = bad || !good;
-          const long long r = record_at(c, good ? page[u][0] : 0, static_cast<int>(at[u][0]), h);
-          pos[u] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Int4*>(c.position + r));
-          order[u] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Float4*>(c.weight + r));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool good = static_cast<unsigned>(page[u][j]) < static_cast<unsigned>(c.num_pages);
-            bad = bad || !good;
-            const int s = min(min(gi + u, g1 - 1) * kGroup + 4 * lane, (L - 1) & ~3) + j;
-            const long long r = record_at(c, good ? page[u][j] : 0, s < L ? static_cast<int>(at[u][j]) : 0, h);
-            pos[u][j] = static_cast<unsigned>(c.position[r]);
-            order[u][j] = __float_as_uint(c.weight[r]);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (gi + u >= g1) break;
-        const int s = (gi + u) * kGroup + 4 * lane;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = static_cast<int>(pos[u][j]);
-          if (s + j < L) newest = max(newest, p);
-          order[u][j] = p < a.keep_first ? 0xffffffffu : weight_order(__uint_as_float(order[u][j]));
-        }
-        keys[(gi + u) * 64 + lane] = order[u];
-        positions[(gi + u) * 64 + lane] = pos[u];
-      }
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) newest = max(newest, __shfl_xor(newest, off, 64));
+    load_records<kFewHold, kQuad>(c, table, h, g0, g1, L, a.keep_first, lane, key, pos, newest, bad);
+    newest = wave_max_i(newest);
     bad = __any(bad);
     if (lane == 0) {
       sh_wave[0][wave] = newest;
@@ -217,7 +331,7 @@ __global__ __launch_bounds__(select_threads(kLds), 4) void evict_select_kernel(E
     for (int x = tid; x < kBins; x += kThreads) sh_hist[x] = 0;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < kFewWaves; ++w) {
       newest = max(newest, sh_wave[0][w]);
       bad = bad || sh_wave[1][w] != 0;
     }
@@ -227,123 +341,221 @@ __global__ __launch_bounds__(select_threads(kLds), 4) void evict_select_kernel(E
       continue;
     }
     const long long recent = static_cast<long long>(newest) - a.keep_last;
+#pragma unroll
+    for (int x = 0; x < kFewHold; ++x) protect(key[x], pos[x], recent);
 
     // The budget-th largest key, from its highest bits down; `left` of the slots with it are kept.
-    unsigned prefix = 0;
+    unsigned threshold = 0;
     int left = a.budget;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const unsigned above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
-      const unsigned bits = pass == 2 ? 1023u : 2047u;
-      for (int gi = g0; gi < g1; gi += 2) {
-        u32x4 key[2], pos[2];
+      const Digit d = digit_of(pass, threshold);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int x = min(gi + u, g1 - 1) * 64 + lane;
-          key[u] = keys[x];
-          if (pass == 0) pos[u] = positions[x];
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (gi + u >= g1) break;
-          const int s = (gi + u) * kGroup + 4 * lane;
-          if (pass == 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (static_cast<int>(pos[u][j]) > recent) key[u][j] = 0xffffffffu;
-            keys[(gi + u) * 64 + lane] = key[u];
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            count_digit(sh_hist, key[u][j] >> shift & bits, s + j < L && (key[u][j] & above) == prefix, lane);
-        }
-      }
+      for (int x = 0; x < kFewHold; ++x)
+        if (g0 + x < g1) count_keys(sh_hist, key[x], (g0 + x) * kGroup + 4 * lane, L, d, lane);
       __syncthreads();
-      // Counts from the highest digit down: a thread has a few digits, and exactly one of all reaches `left`.
-      const int top = kBins - 1 - kMine * tid;
-      int n[kMine], mine = 0;
+      int n[kMine];
 #pragma unroll
       for (int x = 0; x < kMine; ++x) {
-        n[x] = static_cast<int>(sh_hist[top - x]);
-        sh_hist[top - x] = 0;
-        mine += n[x];
+        n[x] = static_cast<int>(sh_hist[kBins - 1 - kMine * tid - x]);
+        sh_hist[kBins - 1 - kMine * tid - x] = 0;
       }
-      const int upto = wave_scan(mine);
-      if (lane == 63) sh_wave[0][wave] = upto;
-      __syncthreads();
-      int before = upto - mine;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) before += w < wave ? sh_wave[0][w] : 0;
-#pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        if (before < left && left <= before + n[x]) {
-          sh_digit = top - x;
-          sh_left = left - before;
-        }
-        before += n[x];
-      }
-      __syncthreads();
-      prefix |= static_cast<unsigned>(sh_digit) << shift;
-      left = sh_left;
+      threshold |= find_digit<kFewWaves>(n, left, sh_wave[0], sh_found, tid, lane, wave) << d.shift;
     }
 
-    // Slots above the threshold and at it before each wave's.
+    // Slots above the threshold and at it before each wave's, then the lists.
     int above = 0, ties = 0;
-    for (int gi = g0; gi < g1; ++gi) {
-      const u32x4 key = keys[gi * 64 + lane];
-      const int s = gi * kGroup + 4 * lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        above += __popcll(__ballot(s + j < L && key[j] > prefix));
-        ties += __popcll(__ballot(s + j < L && key[j] == prefix));
-      }
-    }
-    if (lane == 0) {
+    for (int x = 0; x < kFewHold; ++x)
+      if (g0 + x < g1) count_order(key[x], (g0 + x) * kGroup + 4 * lane, L, threshold, above, ties);
+    above = wave_scan(above);
+    ties = wave_scan(ties);
+    if (lane == 63) {
       sh_wave[0][wave] = above;
       sh_wave[1][wave] = ties;
     }
     __syncthreads();
     above = ties = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < kFewWaves; ++w) {
       above += w < wave ? sh_wave[0][w] : 0;
       ties += w < wave ? sh_wave[1][w] : 0;
     }
-    __syncthreads();
-    for (int gi = g0; gi < g1; ++gi) {
-      const u32x4 key = keys[gi * 64 + lane];
-      const int s = gi * kGroup + 4 * lane;
-      int mine = 0;  // above and (from bit 16 on) at the threshold
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        mine += s + j >= L ? 0 : key[j] > prefix ? 1 : key[j] == prefix ? 0x10000 : 0;
-      const int upto = wave_scan(mine);
-      int g = above + ((upto - mine) & 0xffff), t = ties + ((upto - mine) >> 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = s + j < L, tie = key[j] == prefix;
-        const bool kept = key[j] > prefix || (tie && t < left);
-        const int before = g + min(t, left);
-        if (in && kept && s + j >= a.budget)
-          lists.from[bh * lists.most + lists.most - a.budget + before] = s + j;
-        if (in && !kept && s + j < a.budget) lists.to[bh * lists.most + s + j - before] = s + j;
-        // (the slots below the budget that stay: as many as are not moved to)
-        if (s + j == a.budget - 1) sh_left = before + kept;
-        g += key[j] > prefix;
-        t += tie;
-      }
-      const int all = __builtin_amdgcn_readlane(upto, 63);
-      above += all & 0xffff;
-      ties += all >> 16;
-    }
+    for (int x = 0; x < kFewHold; ++x)
+      if (g0 + x < g1)
+        list_moves(lists, bh, key[x], (g0 + x) * kGroup + 4 * lane, L, threshold, left, a.budget, above, ties,
+                   &sh_stay);
     __syncthreads();
-    const int moves = a.budget - sh_left;
+    const int moves = a.budget - sh_stay;  // (the slots below the budget that stay are not moved to)
     if (tid == 0) lists.count[bh] = moves;
     if (lists.own_moves) {
       if (tid == 0 && h == 0 && a.new_len) a.new_len[b] = a.budget;
-      for (int i = wave * kMoveBatch; i < moves; i += kWaves * kMoveBatch)
+      for (int i = wave * kMoveBatch; i < moves; i += kFewWaves * kMoveBatch)
         move_rows<2>(c, lists, bh, b, h, esize, moves, i, min(kMoveBatch, moves - i), lane);
+    }
+  }
+}
+
+// One pass over many slots; a workgroup has one part of a pair's.
+//   0 records to keys and positions   1, 2, 3 counts of a digit   4 slots above the threshold and at it   5 the lists
+template <int kPass, bool kQuad>
+__global__ __launch_bounds__(64 * kPartWaves) void evict_part_kernel(EvictArgs a, KvArgs c, EvictLists lists) {
+  constexpr int kThreads = 64 * kPartWaves, kMine = kBins / kThreads;
+  __shared__ unsigned sh_hist[kPass >= 1 && kPass <= 3 ? kBins : 1];
+  __shared__ int sh_wave[2][kPartWaves];
+  __shared__ int sh_found[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), part = blockIdx.x;
+  const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
+  const long long pairs = static_cast<long long>(a.B) * c.heads;
+  for (long long bh = blockIdx.y; bh < pairs; bh += gridDim.y) {
+    const int b = static_cast<int>(bh / c.heads), h = static_cast<int>(bh - static_cast<long long>(b) * c.heads);
+    const int L = uniform(a.kv_len[b]);
+    const bool wrong = L < 0 || L > cap;
+    if (wrong || L <= a.budget) {
+      if (kPass == 5 && part == 0 && tid == 0) lists.count[bh] = wrong ? -1 : 0;
+      continue;
+    }
+    // (the last part of L's: it need not be whole; the parts after it only clear counts)
+    const int parts = static_cast<int>((L + kPartSlots - 1LL) / kPartSlots);
+    const int groups = (L - 1) / kGroup + 1, g0 = (part * kPartWaves + wave) * kPartHold;
+    const int g1 = min(groups, g0 + kPartHold);
+    u32x4* far_keys = reinterpret_cast<u32x4*>(lists.keys + bh * lists.slots) + g0 * 64LL + lane;
+    u32x4* far_pos = reinterpret_cast<u32x4*>(lists.positions + bh * lists.slots) + g0 * 64LL + lane;
+    unsigned* hist = lists.hist + bh * 3 * kBins;
+    EvictState* state = lists.state + bh * 3;
+    PartRecord* records = lists.part + bh * lists.parts;
+    if (kPass == 0)
+      for (int x = part * kThreads + tid; x < 3 * kBins; x += lists.parts * kThreads) hist[x] = 0;
+    if (part >= parts) continue;
+    __syncthreads();  // (LDS of the pair before)
+
+    u32x4 key[kPartHold] = {}, pos[kPartHold] = {};
+    if constexpr (kPass == 0) {
+      int newest = -0x7fffffff - 1;
+      bool bad = false;
+      load_records<kPartHold, kQuad>(c, c.table + static_cast<long long>(b) * c.max_pages, h, g0, g1, L, a.keep_first,
+                                     lane, key, pos, newest, bad);
+      newest = wave_max_i(newest);
+      bad = __any(bad);
+#pragma unroll
+      for (int x = 0; x < kPartHold; ++x)
+        if (g0 + x < g1) {
+          far_keys[64 * x] = key[x];
+          far_pos[64 * x] = pos[x];
+        }
+      if (lane == 0) {
+        sh_wave[0][wave] = newest;
+        sh_wave[1][wave] = bad;
+      }
+      __syncthreads();
+      if (tid == 0) {
+#pragma unroll
+        for (int w = 0; w < kPartWaves; ++w) {
+          newest = max(newest, sh_wave[0][w]);
+          bad = bad || sh_wave[1][w] != 0;
+        }
+        records[part] = PartRecord{newest, bad, 0, 0};
+      }
+      continue;
+    }
+
+#pragma unroll
+    for (int x = 0; x < kPartHold; ++x)
+      if (g0 + x < g1) {
+        key[x] = far_keys[64 * x];
+        if (kPass == 1) pos[x] = far_pos[64 * x];
+      }
+    // All parts' records, each wave for itself.
+    int newest = -0x7fffffff - 1, bad = 0, above = 0, ties = 0;
+    for (int x = lane; x < parts; x += 64) {
+      const PartRecord r = records[x];
+      newest = max(newest, r.newest);
+      bad |= r.bad;
+      if (kPass == 5 && x < part) {
+        above += r.above;
+        ties += r.ties;
+      }
+    }
+    if (__any(bad)) {
+      if (kPass == 5 && part == 0 && tid == 0) lists.count[bh] = -1;
+      continue;
+    }
+    unsigned threshold = 0;
+    int left = a.budget;
+    if constexpr (kPass == 1) {
+      const long long recent = static_cast<long long>(wave_max_i(newest)) - a.keep_last;
+#pragma unroll
+      for (int x = 0; x < kPartHold; ++x)
+        if (g0 + x < g1) {
+          protect(key[x], pos[x], recent);
+          far_keys[64 * x] = key[x];
+        }
+    } else if constexpr (kPass == 5) {
+      threshold = state[2].threshold;
+      left = state[2].left;
+    } else {
+      // The digit that the pass before counted, and the state after it for the next one.
+      if (kPass > 2) {
+        threshold = state[kPass - 3].threshold;
+        left = state[kPass - 3].left;
+      }
+      int n[kMine];
+#pragma unroll
+      for (int x = 0; x < kMine; ++x)
+        n[x] = static_cast<int>(hist[(kPass - 2) * kBins + kBins - 1 - kMine * tid - x]);
+      threshold |= find_digit<kPartWaves>(n, left, sh_wave[0], sh_found, tid, lane, wave)
+                   << digit_of(kPass - 2, 0).shift;
+      if (part == 0 && tid == 0) state[kPass - 2] = EvictState{threshold, left};
+    }
+    if constexpr (kPass <= 3) {
+      for (int x = tid; x < kBins; x += kThreads) sh_hist[x] = 0;
+      __syncthreads();
+      const Digit d = digit_of(kPass - 1, threshold);
+#pragma unroll
+      for (int x = 0; x < kPartHold; ++x)
+        if (g0 + x < g1) count_keys(sh_hist, key[x], (g0 + x) * kGroup + 4 * lane, L, d, lane);
+      __syncthreads();
+      for (int x = tid; x < kBins; x += kThreads)
+        if (sh_hist[x]) atomicAdd(&hist[(kPass - 1) * kBins + x], sh_hist[x]);  // (whole numbers: any order)
+    } else {
+      int mine_above = 0, mine_ties = 0;
+#pragma unroll
+      for (int x = 0; x < kPartHold; ++x)
+        if (g0 + x < g1) count_order(key[x], (g0 + x) * kGroup + 4 * lane, L, threshold, mine_above, mine_ties);
+      mine_above = wave_scan(mine_above);
+      mine_ties = wave_scan(mine_ties);
+      if (lane == 63) {
+        sh_wave[0][wave] = mine_above;
+        sh_wave[1][wave] = mine_ties;
+      }
+      __syncthreads();
+      if constexpr (kPass == 4) {
+        if (tid == 0) {
+#pragma unroll
+          for (int w = 0; w < kPartWaves; ++w) {
+            above += sh_wave[0][w];
+            ties += sh_wave[1][w];
+          }
+          records[part].above = above;
+          records[part].ties = ties;
+        }
+      } else {
+        above = __builtin_amdgcn_readlane(wave_scan(above), 63);
+        ties = __builtin_amdgcn_readlane(wave_scan(ties), 63);
+#pragma unroll
+        for (int w = 0; w < kPartWaves; ++w) {
+          above += w < wave ? sh_wave[0][w] : 0;
+          ties += w < wave ? sh_wave[1][w] : 0;
+        }
+        int stay = -1;
+#pragma unroll
+        for (int x = 0; x < kPartHold; ++x)
+          if (g0 + x < g1)
+            list_moves(lists, bh, key[x], (g0 + x) * kGroup + 4 * lane, L, threshold, left, a.budget, above, ties,
+                       &stay);
+        if (stay >= 0) lists.count[bh] = a.budget - stay;  // (the lane of slot budget - 1)
+      }
     }
   }
 }
@@ -363,53 +575,73 @@ __global__ __launch_bounds__(64 * kMoveWaves) void evict_move_kernel(EvictArgs a
   }
 }
 
-template <bool kLds>
-void launch_select(const EvictArgs& a, const KvArgs& c, const EvictLists& lists, unsigned groups, int esize) {
-  const size_t lds = kLds ? 8 * lists.slots : 0;
-  if (c.page_size % 4 == 0)
-    evict_select_kernel<kLds, true><<<groups, select_threads(kLds), lds, a.stream>>>(a, c, lists, esize);
-  else
-    evict_select_kernel<kLds, false><<<groups, select_threads(kLds), lds, a.stream>>>(a, c, lists, esize);
+// The passes, each when the one before has ended.
+template <bool kQuad, int kPass = 0>
+void launch_parts(const EvictArgs& a, const KvArgs& c, const EvictLists& lists, dim3 grid) {
+  evict_part_kernel<kPass, kPass == 0 && kQuad><<<grid, 64 * kPartWaves, 0, a.stream>>>(a, c, lists);
+  if constexpr (kPass < 5) launch_parts<kQuad, kPass + 1>(a, c, lists, grid);
+}
+
+// The workspace's parts in order, and its size.
+size_t lay_out(EvictLists& lists, char* ws, long long pairs, long long capacity, int budget) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = ws + at;
+    at += (bytes + 15) & ~size_t{15};
+    return p;
+  };
+  lists.most = most_moves(capacity, budget);
+  lists.parts = static_cast<int>(part_count(capacity));
+  lists.slots = static_cast<long long>(lists.parts) * kPartSlots;
+  lists.count = reinterpret_cast<int32_t*>(take(pairs * 4));
+  lists.from = reinterpret_cast<int32_t*>(take(pairs * lists.most * 4));
+  lists.to = reinterpret_cast<int32_t*>(take(pairs * lists.most * 4));
+  if (capacity > kFewSlots) {
+    lists.keys = reinterpret_cast<unsigned*>(take(pairs * lists.slots * 4));
+    lists.positions = reinterpret_cast<unsigned*>(take(pairs * lists.slots * 4));
+    lists.hist = reinterpret_cast<unsigned*>(take(pairs * 3 * kBins * 4));
+    lists.state = reinterpret_cast<EvictState*>(take(pairs * 3 * sizeof(EvictState)));
+    lists.part = reinterpret_cast<PartRecord*>(take(pairs * lists.parts * sizeof(PartRecord)));
+  }
+  return at + 16;
 }
 
 }  // namespace
 
 size_t evict_workspace_bytes(int B, int heads, long long capacity, int budget) {
-  const long long pairs = static_cast<long long>(B) * heads, slots = whole_groups(capacity);
-  return align16(pairs * 4) + align16(static_cast<size_t>(pairs) * most_moves(capacity, budget) * 8) +
-         (slots > kLdsSlots ? static_cast<size_t>(pairs) * slots * 8 : 0) + 16;
+  EvictLists lists{};
+  return lay_out(lists, nullptr, static_cast<long long>(B) * heads, capacity, budget);
 }
 
 hipError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, int dtype) {
   const long long pairs = static_cast<long long>(a.B) * c.heads;
   const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
   const int esize = dtype == 0 ? 4 : 2;
-  EvictLists lists;
-  lists.most = most_moves(cap, a.budget);
-  lists.slots = whole_groups(cap);
-  char* ws = static_cast<char*>(a.workspace);
-  lists.count = reinterpret_cast<int32_t*>(ws);
-  ws += align16(pairs * 4);
-  lists.from = reinterpret_cast<int32_t*>(ws);
-  lists.to = lists.from + pairs * lists.most;
-  lists.keys = reinterpret_cast<unsigned*>(ws + align16(static_cast<size_t>(pairs) * lists.most * 8));
+  EvictLists lists{};
+  lay_out(lists, static_cast<char*>(a.workspace), pairs, cap, a.budget);
   lists.magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(c.dim * esize / 8) + 1);
   // (new_len in kv_len's place is written when all workgroups have read kv_len)
   const uintptr_t len = reinterpret_cast<uintptr_t>(a.kv_len), out = reinterpret_cast<uintptr_t>(a.new_len);
   const uintptr_t size = static_cast<uintptr_t>(a.B) * 4;
-  lists.own_moves = lists.most <= kOwnMoves && (!a.new_len || out + size <= len || len + size <= out);
-  const unsigned groups = static_cast<unsigned>(pairs < (1 << 20) ? pairs : 1 << 20);
-  if (lists.slots <= kLdsSlots)
-    launch_select<true>(a, c, lists, groups, esize);
-  else
-    launch_select<false>(a, c, lists, groups, esize);
+  lists.own_moves =
+      cap <= kFewSlots && lists.most <= kOwnMoves && (!a.new_len || out + size <= len || len + size <= out);
+  const unsigned rows = static_cast<unsigned>(pairs < 65535 ? pairs : 65535);
+  if (cap <= kFewSlots) {
+    if (c.page_size % 4 == 0)
+      evict_select_kernel<true><<<rows, 64 * kFewWaves, 0, a.stream>>>(a, c, lists, esize);
+    else
+      evict_select_kernel<false><<<rows, 64 * kFewWaves, 0, a.stream>>>(a, c, lists, esize);
+  } else {
+    const dim3 grid(lists.parts, rows);
+    c.page_size % 4 == 0 ? launch_parts<true>(a, c, lists, grid) : launch_parts<false>(a, c, lists, grid);
+  }
   if (!lists.own_moves) {
     // About 16384 waves, or as many as there can be batches.
     const long long need = (lists.most + kMoveWaves * kMoveBatch - 1) / (kMoveWaves * kMoveBatch);
     long long chunks = 4096 / pairs;
     if (chunks > need) chunks = need;
     if (chunks < 1) chunks = 1;
-    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(pairs < 65535 ? pairs : 65535));
+    const dim3 grid(static_cast<unsigned>(chunks), rows);
     evict_move_kernel<<<grid, 64 * kMoveWaves, 0, a.stream>>>(a, c, lists, esize);
   }
   return hipGetLastError();

@@ -9,8 +9,8 @@
 // memory to registers.  The query rows, which all slots of a segment (one sequence and kv head) share, lie in LDS
 // operand by operand.  (Plain loads: streaming ones, which are faster where nothing is written, took 543 us for
 // 64 x 16380 slots of 8 heads where plain ones take 481, 391 of them without the weights' stores; holding stores back
-// in LDS for 4-16 tiles changed that by 1%.)  The tiles of all segments, laid end to end and weighed by what they cost, are cut into
-// equal ranges, one a workgroup, whose four waves take the range's tiles in turn.
+// in LDS for 4-16 tiles changed that by 1%.)  The tiles of all segments, laid end to end and weighed by what they
+// cost, are cut into equal ranges, one a workgroup, whose four waves take the range's tiles in turn.
 #include <hip/hip_runtime.h>
 
 #include "paged.h"
