@@ -146,6 +146,8 @@ def prepare(case, seed):
         import speculative_decoding_verification_specdec_amd as specdec
         s["lib"] = specdec
         s["cache"] = specdec.PagedKvCache(s["k"], s["v"], s["table"], weight=s["weight"], position=s["position"])
+        if case["op"] == "weights":  # dense, as the call takes it (one head a group: the plain form's is a transposed view)
+            s["lse"] = s["lse"].contiguous()
         if case["op"] == "attend":
             s["workspace"] = specdec.new_paged_attention_workspace(s["cache"], K, H)
         if case["op"] == "evict":
