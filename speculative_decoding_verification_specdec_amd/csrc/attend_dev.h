@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attend_plan.h"
 #include "paged_tiles.h"
 #include "wave_ops.h"
@@ -63,19 +65,25 @@ struct AttendPiece {
   const int32_t* table;       // of the sequence
 };
 
-template <typename T, int kDim, bool kFast, int kRowTiles, bool kQueryLds>
+template <typename T, int kDim, bool kFast, int kRowTiles, bool kQueryLds, bool kShared = false>
 struct AttendWave {
   typedef Tile<T, kDim, kFast> L;
   // kQueryLds: the query operands are read from LDS for each tile instead of staying in registers.
   static constexpr int kQueryTiles = kQueryLds ? 1 : kRowTiles;
+  // kShared: the operands of K and V are read from the workgroup's tile in LDS step by step; of V two words of each
+  // row at a time, which make kPair groups of the output.
+  static constexpr int kPairs = L::kWords / 2, kPair = L::kOut / kPairs;
 
   const KvArgs& c;
   int page_shift, lane, col, g;
   float scale;
   u32x4 (*sh_q)[64];        // [row tile * steps][lane]
   u32x4 q[kQueryTiles][L::kSteps];
-  u32x4 kf[L::kSub][L::kSteps];
-  unsigned vf[L::kRowsV][L::kWords];
+  u32x4 kf[kShared ? 1 : L::kSub][kShared ? 1 : L::kSteps];
+  unsigned vf[kShared ? 1 : L::kRowsV][kShared ? 1 : L::kWords];
+  const u32x4 (*sh_k)[64];  // [sub * steps][lane]
+  const u32x2 (*sh_v)[64];  // [pair * rows][lane]
+  u32x2 vp[kShared ? L::kRowsV : 1];
   f32x4 o[kRowTiles][L::kOut];
   float m[kRowTiles], l[kRowTiles];
   int limit[kRowTiles];     // last slot that the lane's row sees
@@ -162,8 +170,11 @@ struct AttendWave {
       for (int t = 0; t < kRowTiles; ++t) {
         const u32x4 qt = kQueryLds ? sh_q[t * L::kSteps + e][lane] : q[kQueryLds ? 0 : t][e];
 #pragma unroll
-        for (int sub = 0; sub < L::kSub; ++sub) p[t][sub] = mma16(kf[sub][e], qt, p[t][sub], T{});
-        if (kQueryLds && t == kRowTiles - 1) __builtin_amdgcn_sched_barrier(0);  // (one step's operands at a time)
+        for (int sub = 0; sub < L::kSub; ++sub)
+          p[t][sub] = mma16(kShared ? sh_k[sub * L::kSteps + e][lane] : kf[kShared ? 0 : sub][kShared ? 0 : e], qt,
+                            p[t][sub], T{});
+        // (few steps' operands at a time)
+        if ((kQueryLds || (kShared && e % 2 == 1)) && t == kRowTiles - 1) __builtin_amdgcn_sched_barrier(0);
       }
   }
 
@@ -210,6 +221,19 @@ struct AttendWave {
     }
   }
 
+  // The words of V for output groups kPair * pair on; a word of a row.
+  __device__ __forceinline__ void fetch_pair(int pair) {
+    if constexpr (kShared)
+#pragma unroll
+      for (int row = 0; row < L::kRowsV; ++row) vp[row] = sh_v[pair * L::kRowsV + row][lane];
+  }
+  __device__ __forceinline__ unsigned word(int row, int w) const {
+    if constexpr (kShared)
+      return vp[row][w & 1];
+    else
+      return vf[row][w];
+  }
+
   // acc + V^T P^T for output group x of one row tile; p the probabilities by (sub, r), packed for the
   // 16-bit types.  `keep`, where given, has the bits of the operands' slots that count.
   template <bool kMasked>
@@ -221,14 +245,14 @@ struct AttendWave {
       u32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i] = __builtin_amdgcn_perm(vf[2 * i + 1][x / 2], vf[2 * i][x / 2], select);
+        v[i] = __builtin_amdgcn_perm(word(2 * i + 1, x / 2), word(2 * i, x / 2), select);
       return kMasked ? mma16(v & keep, packed & keep, acc, T{}) : mma16(v, packed, acc, T{});
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const unsigned pr = __float_as_uint(p[0][r]);
         acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
-            __uint_as_float(kMasked ? vf[r][x] & keep[r] : vf[r][x]),
+            __uint_as_float(kMasked ? word(r, x) & keep[r] : word(r, x)),
             __uint_as_float(kMasked ? pr & keep[r] : pr), acc, 0, 0, 0);
       }
       return acc;
@@ -254,9 +278,12 @@ struct AttendWave {
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) pk[t] = packed(p[t]);
 #pragma unroll
-    for (int x = 0; x < L::kOut; ++x)
+    for (int x = 0; x < L::kOut; ++x) {
+      if (x % kPair == 0) fetch_pair(x / kPair);
+      if (kShared && x % kPair == 0) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < kRowTiles; ++t) o[t][x] = product<false>(p[t], pk[t], x, u32x4{}, o[t][x]);
+    }
   }
 
   static __device__ __forceinline__ bool word_finite(unsigned w) {
@@ -272,9 +299,13 @@ struct AttendWave {
   __device__ __forceinline__ void products_edge(const f32x4 (&p)[kRowTiles][L::kSub], int first, int len, int total) {
     bool finite = true;
 #pragma unroll
-    for (int x = 0; x < L::kRowsV; ++x)
+    for (int pair = 0; pair < kPairs; ++pair) {
+      fetch_pair(pair);
+      if (kShared) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int y = 0; y < L::kWords; ++y) finite = finite && word_finite(vf[x][y]);
+      for (int x = 0; x < L::kRowsV; ++x)
+        finite = finite && word_finite(word(x, 2 * pair)) && word_finite(word(x, 2 * pair + 1));
+    }
     const bool at_once = !__any(!finite);
     u32x4 pk[kRowTiles];
 #pragma unroll
@@ -298,6 +329,8 @@ struct AttendWave {
         const bool sees = at_once || only <= limit[t];
 #pragma unroll
         for (int x = 0; x < L::kOut; ++x) {
+          if (x % kPair == 0) fetch_pair(x / kPair);
+          if (kShared) __builtin_amdgcn_sched_barrier(0);
           const f32x4 add = product<true>(p[t], pk[t], x, keep, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[t][x][r] += sees ? add[r] : 0.f;
@@ -814,23 +847,27 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
   }
 }
 
-// The same for many rows: waves with 16 or 32 rows each share every tile of K and V through LDS; the next tile is
-// on its way in registers while this one is computed on.  A tile lies in LDS operand by operand, 64 lanes x 16
-// bytes as the matrix instructions take them, so that it is written and read in order, without bank conflicts.
+// The same for many rows: four waves with 16 or 32 rows each share every tile of K and V through LDS; the next tile
+// is on its way in registers while this one is computed on.  A tile lies in LDS operand by operand, 64 lanes x 16
+// or 8 bytes as the matrix instructions take them, so that it is written and read in order, without bank conflicts,
+// and is read as it is needed: whole operands in registers left no room for 32 rows a wave, which halve the bytes
+// read from LDS for each product (64 tokens of 32 heads on 4 kv heads over 44 x 416-3329 slots of float16: head
+// dim 128 277 -> 217 us, 256 859 -> 558 us, 310 TFLOP/s).
 // (Two tiles a barrier took 650 us for 64 rows over 64 x 8-16k slots where one takes 596; two tiles ahead in
 // registers 648; 16 rows a wave 648 where 64 rows in one wave took 588-670.)
 template <typename T, int kDim, bool kFast, int kRowTiles, int kWaves>
-__global__ __launch_bounds__(64 * kWaves, kDim == 256 ? 1 : 2) void attend_wide_kernel(AttendArgs a, KvArgs c,
-                                                                                       AttendPlan plan) {
+__global__ __launch_bounds__(64 * kWaves, kDim == 256 && kRowTiles == 2 ? 1 : 2) void attend_wide_kernel(
+    AttendArgs a, KvArgs c, AttendPlan plan) {
   typedef Tile<T, kDim, kFast> L;
-  typedef AttendWave<T, kDim, kFast, kRowTiles, false> Wave;
+  typedef AttendWave<T, kDim, kFast, kRowTiles, false, true> Wave;
   constexpr int kStepsK = L::kSub * L::kSteps;     // K operands a tile, a wave's share of them to load
   constexpr int kStepsV = L::kRowsV * L::kLoadsV;  // V loads a tile, likewise
   constexpr int kMineK = kStepsK / kWaves, kMineV = kStepsV / kWaves;
   typedef typename L::LoadV VecV;
   extern __shared__ float sh_parts[];
-  u32x4* sh_k = reinterpret_cast<u32x4*>(sh_parts);               // [2][kStepsK][64]
-  VecV* sh_v = reinterpret_cast<VecV*>(sh_k + 2 * kStepsK * 64);  // [2][kStepsV][64]
+  constexpr int kPlanes = L::kRowsV * Wave::kPairs;
+  u32x4(*sh_k)[64] = reinterpret_cast<u32x4(*)[64]>(sh_parts);              // [2][kStepsK]
+  u32x2(*sh_v)[64] = reinterpret_cast<u32x2(*)[64]>(sh_k + 2 * kStepsK);    // [2][kPlanes]
   __shared__ int sh_bad[kWaves];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -925,45 +962,47 @@ __global__ __launch_bounds__(64 * kWaves, kDim == 256 ? 1 : 2) void attend_wide_
     auto put = [&](int buffer) __attribute__((always_inline)) {
 #pragma unroll
       for (int y = 0; y < kMineK; ++y)
-        sh_k[(buffer * kStepsK + wave * kMineK + y) * 64 + lane] = mine_k[y];
+        sh_k[buffer * kStepsK + wave * kMineK + y][lane] = mine_k[y];
 #pragma unroll
-      for (int y = 0; y < kMineV; ++y) sh_v[(buffer * kStepsV + step_v + y) * 64 + lane] = mine_v[y];
+      for (int y = 0; y < kMineV; ++y)
+#pragma unroll
+        for (int e = 0; e < L::kLoadWords / 2; ++e) {
+          const int row = (step_v + y) / L::kLoadsV, pair = (step_v + y) % L::kLoadsV * (L::kLoadWords / 2) + e;
+          sh_v[buffer * kPlanes + pair * L::kRowsV + row][lane] = u32x2{mine_v[y][2 * e], mine_v[y][2 * e + 1]};
+        }
     };
 
     find(now.first);
     fetch();
     find(now.first + 1);
     put(0);
-    for (int tile = now.first, buffer = 0; tile < now.end; ++tile, buffer ^= 1) {
+    // (two loops, as in the split kernel: with both kinds of tile in one the compiler keeps two copies of the outputs)
+    auto step = [&](int tile, int buffer, auto edge) __attribute__((always_inline)) {
       fetch();
       find(tile + 2);
       // All waves' parts of this buffer are written, and the other buffer's are read.  (LDS alone is waited
       // for: the loads above stay in flight.)
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (wave_row < now.n * group) {
-#pragma unroll
-        for (int y = 0; y < kStepsK; ++y)
-          s.kf[y / L::kSteps][y % L::kSteps] = sh_k[(buffer * kStepsK + y) * 64 + lane];
+        s.sh_k = sh_k + buffer * kStepsK;
+        s.sh_v = sh_v + buffer * kPlanes;
         f32x4 p[kRowTiles][L::kSub];
         s.scores(p);
-#pragma unroll
-        for (int y = 0; y < kStepsV; ++y) {
-          const VecV v = sh_v[(buffer * kStepsV + y) * 64 + lane];
-#pragma unroll
-          for (int e = 0; e < L::kLoadWords; ++e) s.vf[y / L::kLoadsV][y % L::kLoadsV * L::kLoadWords + e] = v[e];
-        }
-        const int first = tile * L::kKeys;
-        if (first + L::kKeys - 1 > now.len) {
-          s.mask(p, first);
+        if constexpr (decltype(edge)::value) {
+          s.mask(p, tile * L::kKeys);
           s.softmax(p);
-          s.products_edge(p, first, now.len, now.len + now.n);
+          s.products_edge(p, tile * L::kKeys, now.len, now.len + now.n);
         } else {
           s.softmax(p);
           s.products(p);
         }
       }
       put(buffer ^ 1);
-    }
+    };
+    const int whole_end = min(now.end, (now.len + 1) / L::kKeys);  // every row sees every slot
+    int tile = now.first, buffer = 0;
+    for (; tile < whole_end; ++tile, buffer ^= 1) step(tile, buffer, std::false_type{});
+    for (; tile < now.end; ++tile, buffer ^= 1) step(tile, buffer, std::true_type{});
 
     const bool begins = now.first == 0, whole = begins && now.end == now.tiles;
     const int slot = begins ? 1 : 0;
@@ -1030,9 +1069,7 @@ void launch_attend_dim(const AttendArgs& a, const KvArgs& c, const AttendPlan& p
     constexpr unsigned kLds = 2 * 2 * Tile<T, kDim, kFast>::kKeys * kDim * sizeof(T);  // two tiles of K and V
     if (p.rows == 64)
       attend_wide_kernel<T, kDim, kFast, 1, 4><<<groups, 256, kLds, a.stream>>>(a, c, p);
-    else if constexpr (kDim == 128)
-      attend_wide_kernel<T, kDim, kFast, 1, 8><<<groups, 512, kLds, a.stream>>>(a, c, p);
-    else if constexpr (kDim == 64)
+    else
       attend_wide_kernel<T, kDim, kFast, 2, 4><<<groups, 256, kLds, a.stream>>>(a, c, p);
   } else if constexpr (kDim == 256) {
     attend_split_kernel<T, kDim, kFast, 1, 1><<<groups, 64, 0, a.stream>>>(a, c, p);

@@ -20,16 +20,17 @@ namespace {
 
 // Up to 32 rows (16 of the widest heads, as their registers allow) every wave takes all rows of its own range:
 // 1024 ranges, one wave a SIMD, four of them a workgroup where the LDS holds their parts.  More rows are shared
-// out to the waves of a workgroup, 64 or 128 a chunk, with a range for each workgroup that is resident: 512, or
-// 256 where eight waves or the LDS allow one a CU.
+// out to the four waves of a workgroup, 64 or 128 a chunk, with a range for each workgroup that is resident: 512, or
+// 256 where 128 rows of the widest heads allow one a CU (64 rows at 256 ranges: 157 us where 512 take 152, 64 x
+// 500-4000 slots of 4 heads; 128 rows against 64 in two workgroups a CU: 558 and 697 us, 512 rows in all).
 AttendPlan make_plan(int K, int q_heads, int kv_heads, int dim) {
   AttendPlan p{};
   const int rows = (K + 1) * (q_heads / kv_heads);
   p.dim = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   p.wide = rows > (p.dim == 256 ? 16 : 32);
   if (p.wide) {
-    p.rows = rows <= 64 || p.dim == 256 ? 64 : 128;
-    p.log_ranges = p.dim == 256 || (p.dim == 128 && p.rows == 128) ? 8 : 9;
+    p.rows = rows <= 64 ? 64 : 128;
+    p.log_ranges = p.dim == 256 && p.rows == 128 ? 8 : 9;
   } else {
     p.rows = rows <= 16 ? 16 : 32;
     p.log_ranges = 10;
