@@ -397,9 +397,9 @@ typedef struct {
   int32_t dtype;              /* specdec_dtype                                                     */
   int32_t num_pages;          /* pages in the pool; num_pages * page_size < 2^31                    */
   int32_t page_size;          /* slots a page, >= 1                                                */
-  int32_t num_kv_heads;       /* >= 1                                                              */
+  int32_t num_kv_heads;       /* 1 .. 65536                                                        */
   int32_t head_dim;           /* a multiple of 8, 8 .. SPECDEC_MAX_HEAD_DIM                         */
-  int32_t max_pages;          /* entries of a row of page_table; max_pages * page_size < 2^31       */
+  int32_t max_pages;          /* entries of a row of page_table; max_pages * page_size <= 2^30      */
   int64_t page_stride;        /* in elements, each >= head_dim (where the count is over 1)          */
   int64_t slot_stride;
   int64_t head_stride;

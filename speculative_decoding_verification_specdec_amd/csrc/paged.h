@@ -1,5 +1,5 @@
 // Internal interface of the paged-cache entry points: host code in paged_api.cpp, kernels in
-// rope.hip, paged_attention.hip, kv_weights.hip and kv_evict.hip.
+// rope.hip, attend_*.hip (their plan in paged_attention.cpp), kv_weights.hip and kv_evict.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -11,7 +11,7 @@ namespace specdec {
 constexpr int kMaxHeadDim = 256;
 
 // The cache of include/specdec.h as the kernels take it.  Sizes were checked on the host:
-// num_pages * page_size and max_pages * page_size are below 2^31.
+// num_pages * page_size is below 2^31, max_pages * page_size (slots a sequence can have) at most 2^30.
 struct KvArgs {
   char* k;
   char* v;

@@ -35,10 +35,11 @@ bool rows_valid(int32_t B, int32_t K, int32_t heads) {
 
 specdec_status check_cache(const specdec_kv_cache* c) {
   if (!c) return SPECDEC_ERR_NULL;
-  const long long limit = 1LL << 31;
-  if (c->num_pages < 1 || c->page_size < 1 || c->num_kv_heads < 1 || c->max_pages < 1 ||
-      !dim_valid(c->head_dim) || static_cast<long long>(c->num_pages) * c->page_size >= limit ||
-      static_cast<long long>(c->max_pages) * c->page_size >= limit)
+  // (slots of a sequence: the kernels round them up to whole tiles and groups, in 32 bits)
+  if (c->num_pages < 1 || c->page_size < 1 || c->num_kv_heads < 1 || c->num_kv_heads > 65536 ||
+      c->max_pages < 1 || !dim_valid(c->head_dim) ||
+      static_cast<long long>(c->num_pages) * c->page_size >= (1LL << 31) ||
+      static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30))
     return SPECDEC_ERR_SHAPE;
   if (c->dtype != SPECDEC_F32 && c->dtype != SPECDEC_BF16 && c->dtype != SPECDEC_F16)
     return SPECDEC_ERR_DTYPE;

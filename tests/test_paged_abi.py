@@ -232,3 +232,13 @@ def test_binding_checks_the_round():
                 lambda: specdec_rope_append(q, kn, kn, c, kv, None, out=q.float())):
         with pytest.raises(SpecdecError):
             bad()
+
+
+@pytest.mark.parametrize("call", [call_rope, call_attend, call_weights, call_evict])
+def test_limits_of_a_cache(lib, call):
+    # 2^30 slots a sequence and 65536 kv heads; one more of either would pass 32 bits in a kernel.
+    # (An empty batch: nothing is launched.)
+    most = dict(page_size=1 << 20, max_pages=1 << 10, slot_stride=64, page_stride=64 << 20, num_kv_heads=1)
+    assert call(lib, cache(**most), B=0, heads=1) == 0 if call is not call_evict else call(lib, cache(**most), B=0) == 0
+    assert call(lib, cache(**{**most, "max_pages": (1 << 10) + 1}), B=0, kv=FAKE) == -2
+    assert call(lib, cache(num_kv_heads=65537, slot_stride=64 * 65537, page_stride=1024 * 65537)) == -2
