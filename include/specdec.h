@@ -452,7 +452,8 @@ specdec_status specdec_rope_frequencies(int32_t rotary_dim, double base, int32_t
  * first_pos   [B]    int32 position of each sequence's first new token (the following ones count up);
  *             NULL = kv_len (right until the cache evicts; afterwards seq_len - 1).  A sequence
  *             whose positions are negative or pass 2^31 - 1 is invalid.
- * q_out       [B, K+1, num_q_heads, head_dim] dense, out; may be q itself if q is dense.
+ * q_out       [B, K+1, num_q_heads, head_dim] dense, out; may be q itself if q is dense
+ *             (SPECDEC_ERR_SHAPE if it is not).
  * cache       k, v rows of the new slots are written; also weight (0) and position where given.
  * A new token whose page id is outside the pool gets a NaN q_out row and writes nothing, the
  * sequence's other tokens are done.  No workspace. */

@@ -146,10 +146,15 @@ specdec_status specdec_rope_append(const void* q, const void* k, const void* v, 
   if (st != SPECDEC_OK) return st;
   if (!rope) return SPECDEC_ERR_NULL;
   const int32_t dim = cache->head_dim, kv_heads = cache->num_kv_heads;
-  if (num_q_heads < 1 || !rows_valid(B, K, num_q_heads) || rope->rotary_dim < 0 ||
+  if (num_q_heads < 1 || !rows_valid(B, K, num_q_heads) ||
+      num_q_heads + 2LL * kv_heads >= (1LL << 31) || rope->rotary_dim < 0 ||
       rope->rotary_dim % 2 || rope->rotary_dim > dim || !isfinite(rope->scale) ||
       !stride_valid(q_stride, B, K, num_q_heads, dim) ||
       !stride_valid(k_stride, B, K, kv_heads, dim) || !stride_valid(v_stride, B, K, kv_heads, dim))
+    return SPECDEC_ERR_SHAPE;
+  // (in place only where every row of q_out is its own row of q)
+  if (B > 0 && q && q_out == q && static_cast<long long>(B) * (K + 1LL) > 1 &&
+      q_stride != static_cast<long long>(num_q_heads) * dim)
     return SPECDEC_ERR_SHAPE;
   if (B == 0) return SPECDEC_OK;
   st = check_cache_pointers(cache);

@@ -242,3 +242,9 @@ def test_limits_of_a_cache(lib, call):
     assert call(lib, cache(**most), B=0, heads=1) == 0 if call is not call_evict else call(lib, cache(**most), B=0) == 0
     assert call(lib, cache(**{**most, "max_pages": (1 << 10) + 1}), B=0, kv=FAKE) == -2
     assert call(lib, cache(num_kv_heads=65537, slot_stride=64 * 65537, page_stride=1024 * 65537)) == -2
+
+
+def test_rope_in_place_wants_a_dense_q(lib):
+    # q_out = q with tokens further apart than their rows: a token's output would lie in another's input.
+    assert call_rope(lib, q=2 * FAKE, qo=2 * FAKE, qs=1024) == -2
+    assert call_rope(lib, q=2 * FAKE, qo=2 * FAKE, qs=1024, heads=2 ** 31 - 1, B=1, K=0) == -2
