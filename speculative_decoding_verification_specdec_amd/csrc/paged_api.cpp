@@ -152,10 +152,6 @@ specdec_status specdec_rope_append(const void* q, const void* k, const void* v, 
       !stride_valid(q_stride, B, K, num_q_heads, dim) ||
       !stride_valid(k_stride, B, K, kv_heads, dim) || !stride_valid(v_stride, B, K, kv_heads, dim))
     return SPECDEC_ERR_SHAPE;
-  // (in place only where every row of q_out is its own row of q)
-  if (B > 0 && q && q_out == q && static_cast<long long>(B) * (K + 1LL) > 1 &&
-      q_stride != static_cast<long long>(num_q_heads) * dim)
-    return SPECDEC_ERR_SHAPE;
   if (B == 0) return SPECDEC_OK;
   st = check_cache_pointers(cache);
   if (st == SPECDEC_ERR_NULL) return st;
@@ -168,6 +164,10 @@ specdec_status specdec_rope_append(const void* q, const void* k, const void* v, 
       stride_misaligned(k_stride, B, K, cache->dtype) ||
       stride_misaligned(v_stride, B, K, cache->dtype))
     return SPECDEC_ERR_ALIGN;
+  // (in place only where every row of q_out is its own row of q)
+  if (q_out == q && static_cast<long long>(B) * (K + 1LL) > 1 &&
+      q_stride != static_cast<long long>(num_q_heads) * dim)
+    return SPECDEC_ERR_SHAPE;
   specdec::RopeArgs a{};
   a.q = q;
   a.k = k;
