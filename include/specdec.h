@@ -514,7 +514,8 @@ specdec_status specdec_kv_weights(const void* q, int64_t q_stride, const float* 
  *             the lower slots are kept.)
  * new_len     [B] out int32 min(L, budget), or -1 for an invalid sequence (L outside [0, max_pages *
  *             page_size] or a page id of its slots outside the pool), of which nothing moves; NULL
- *             = not wanted.  It may be kv_len itself (in the last layer's call).
+ *             = not wanted.  It may be kv_len itself (in the last layer's call), but
+ *             not lie across it (SPECDEC_ERR_SHAPE).
  * workspace   device scratch of >= specdec_kv_evict_workspace_size() bytes, 16-byte aligned, no
  *             initialisation needed; calls that overlap in time need their own.
  * cache->weight and cache->position are required. */

@@ -621,10 +621,7 @@ hipError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, int dtype) {
   lay_out(lists, static_cast<char*>(a.workspace), pairs, cap, a.budget);
   lists.magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(c.dim * esize / 8) + 1);
   // (new_len in kv_len's place is written when all workgroups have read kv_len)
-  const uintptr_t len = reinterpret_cast<uintptr_t>(a.kv_len), out = reinterpret_cast<uintptr_t>(a.new_len);
-  const uintptr_t size = static_cast<uintptr_t>(a.B) * 4;
-  lists.own_moves =
-      cap <= kFewSlots && lists.most <= kOwnMoves && (!a.new_len || out + size <= len || len + size <= out);
+  lists.own_moves = cap <= kFewSlots && lists.most <= kOwnMoves && a.new_len != a.kv_len;
   const unsigned rows = static_cast<unsigned>(pairs < 65535 ? pairs : 65535);
   if (cap <= kFewSlots) {
     if (c.page_size % 4 == 0)

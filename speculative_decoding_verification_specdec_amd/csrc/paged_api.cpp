@@ -293,6 +293,10 @@ specdec_status specdec_kv_evict(const specdec_kv_cache* cache, const int32_t* kv
   if (st != SPECDEC_OK) return st;
   if (misaligned(kv_len, 4) || misaligned(new_len, 4) || misaligned(workspace, 16))
     return SPECDEC_ERR_ALIGN;
+  // new_len is kv_len or lies apart from it: a sequence's length is read while others' are written.
+  const uintptr_t len = reinterpret_cast<uintptr_t>(kv_len), out = reinterpret_cast<uintptr_t>(new_len);
+  const uintptr_t bytes = static_cast<uintptr_t>(B) * 4;
+  if (new_len && out != len && out < len + bytes && len < out + bytes) return SPECDEC_ERR_SHAPE;
   if (workspace_bytes < specdec_kv_evict_workspace_size(B, cache, budget))
     return SPECDEC_ERR_WORKSPACE;
   specdec::EvictArgs a{};

@@ -248,3 +248,10 @@ def test_rope_in_place_wants_a_dense_q(lib):
     # q_out = q with tokens further apart than their rows: a token's output would lie in another's input.
     assert call_rope(lib, q=2 * FAKE, qo=2 * FAKE, qs=1024) == -2
     assert call_rope(lib, q=2 * FAKE, qo=2 * FAKE, qs=1024, heads=2 ** 31 - 1, B=1, K=0) == -2
+
+
+def test_evict_wants_new_len_apart_from_kv_len_or_in_its_place(lib):
+    for off in (-8, -4, 4, 8):
+        assert call_evict(lib, kv=2 * FAKE, new=2 * FAKE + off) == -2
+    for off in (0, -12, 12):            # (told apart by the next check)
+        assert call_evict(lib, kv=2 * FAKE, new=2 * FAKE + off, wsb=8) == -5
