@@ -1,0 +1,254 @@
+"""The paged-cache entry points on the GPU where their kernels change over: batches of more sequences than a wave
+has lanes, many query rows, caches of more slots than a workgroup holds, workspaces that captured graphs share.
+Against the float64 oracle; tolerances as in test_gpu_paged.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as po
+from paged_cases import make_round, wide
+from speculative_decoding_verification_specdec_amd import (
+    PagedKvCache, new_kv_evict_workspace, new_paged_attention_workspace, specdec_kv_evict, specdec_kv_weights,
+    specdec_paged_attention, specdec_rope_append)
+from test_gpu_paged import DEV, arrays, cache_of, check_attention, dev, evict_case, nd_of, same_bits
+
+pytestmark = pytest.mark.gpu
+
+
+# lens, K, heads, kv_heads, dim, page, dtype, ragged: 33 to 64 rows and more, whole and odd pages and head sizes
+MANY_ROWS = [
+    ([300, 77, 0], 11, 16, 4, 64, 16, "bf16", True), ([500, 30], 23, 16, 4, 64, 24, "f16", True),
+    ([260], 40, 8, 2, 128, 16, "bf16", False), ([133, 700], 15, 16, 4, 96, 7, "f16", True),
+    ([200, 64], 9, 12, 2, 256, 16, "bf16", True), ([200, 321], 31, 8, 1, 256, 32, "f16", False),
+    ([100, 90], 20, 8, 1, 200, 10, "f32", True), ([150, 31], 12, 16, 4, 128, 16, "f32", False),
+    ([150, 20], 30, 8, 2, 128, 8, "f32", True), ([90] * 70, 9, 8, 2, 64, 16, "bf16", True),
+    ([40, 31, 32], 50, 3, 3, 128, 16, "bf16", True), ([30, 15, 16], 33, 4, 2, 256, 16, "f32", True),
+]
+
+
+@pytest.mark.parametrize("lens,K,heads,kv_heads,dim,page,dtype,ragged", MANY_ROWS)
+def test_attention_of_many_rows(lens, K, heads, kv_heads, dim, page, dtype, ragged):
+    print(f"\n[case] many rows {lens[:4]} K={K} {heads}/{kv_heads} D={dim} page={page} {dtype}", flush=True)
+    r = make_round(lens, K, heads, kv_heads, dim, page, dtype, seed=K + dim, ragged=ragged)
+    out, lse = specdec_paged_attention(dev(r.q), cache_of(r, head_major=page % 3 == 1), dev(r.kv_len),
+                                       num_draft=dev(r.num_draft), scale=r.scale, want_lse=True)
+    check_attention(r, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K,heads,dim,length", [(5, 8, 128, 60), (15, 8, 128, 90), (31, 8, 128, 64), (3, 8, 256, 30),
+                                                (12, 8, 256, 61), (40, 8, 256, 33), (20, 4, 80, 48)])
+def test_attention_later_values_stay_out_of_earlier_rows(K, heads, dim, length, dtype):
+    # Draft 2's value row holds every kind of value that is not finite; the rows before it do not see them.
+    print(f"\n[case] later values K={K} D={dim} {dtype}", flush=True)
+    r = make_round([length], K, heads, 2, dim, 16, dtype, seed=160 + K)
+    want = po.paged_attention(*arrays(r), scale=r.scale)
+    j = length + 2
+    row = r.v[int(r.table[0, j // 16]), j % 16]
+    row[:, 0::3], row[:, 1::3], row[:, 2::3] = float("nan"), float("inf"), -float("inf")
+    out, lse = specdec_paged_attention(dev(r.q), cache_of(r), dev(r.kv_len), scale=r.scale, want_lse=True)
+    few = type(r)(**{**r.__dict__, "q": r.q[:, :2].contiguous()})
+    check_attention(few, out[:, :2].cpu(), lse[:, :2].cpu(), [x[:, :2] for x in want])
+    assert torch.isnan(out[:, 2:, :, 0]).all() and not torch.isfinite(out[:, 2:]).any()
+
+
+def test_attention_of_many_rows_with_a_bad_page():
+    r = make_round([900, 700, 40], 11, 16, 2, 128, 16, "bf16", seed=161)
+    r.table[1, 20] = r.k.shape[0]
+    out, lse = specdec_paged_attention(dev(r.q), cache_of(r), dev(r.kv_len), scale=r.scale, want_lse=True)
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    check_attention(r, out, lse)
+
+
+def many_sequences(B, K, heads, dim, page, dtype, seed):
+    # Lengths 0 to 39, every seventh sequence invalid in one of four ways.
+    r = make_round([(7 * i) % 40 for i in range(B)], K, heads, 2, dim, page, dtype, seed=seed, ragged=True)
+    kv, nd = r.kv_len.clone(), r.num_draft.clone()
+    for b in range(0, B, 28):
+        kv[b] = -1
+    for b in range(7, B, 28):
+        nd[b] = K + 1
+    for b in range(14, B, 28):
+        nd[b] = -1
+    for b in range(21, B, 28):
+        kv[b] = 10 ** 9
+    return type(r)(**{**r.__dict__, "kv_len": kv, "num_draft": nd})
+
+
+@pytest.mark.parametrize("B,K,heads,dim,page,dtype", [(64, 3, 4, 64, 16, "bf16"), (65, 3, 4, 128, 5, "f16"),
+                                                      (150, 1, 8, 64, 16, "f32"), (1100, 0, 2, 64, 4, "bf16"),
+                                                      (130, 9, 8, 64, 16, "bf16")])
+def test_batches_of_many_sequences(B, K, heads, dim, page, dtype):
+    print(f"\n[case] B={B} K={K} D={dim} {dtype}", flush=True)
+    r = many_sequences(B, K, heads, dim, page, dtype, seed=170 + B)
+    c = cache_of(r)
+    out, lse = specdec_paged_attention(dev(r.q), c, dev(r.kv_len), num_draft=dev(r.num_draft), scale=r.scale,
+                                       want_lse=True)
+    check_attention(r, out, lse)
+    # The weights of the same round, with the oracle's lse; accept_len also outside [0, k_b].
+    accept = torch.tensor([i % (K + 3) - 1 for i in range(B)], dtype=torch.int32)
+    q, k, v, table, kv = arrays(r)
+    ref_lse = po.paged_attention(q, k, v, table, kv, num_draft=nd_of(r), scale=r.scale)[1].astype(np.float32)
+    specdec_kv_weights(dev(r.q), dev(torch.from_numpy(ref_lse)), c, dev(r.kv_len), num_draft=dev(r.num_draft),
+                       accept_len=dev(accept), scale=r.scale)
+    ref, added, size = po.kv_weights(q, ref_lse, k, table, kv, wide(r.weight), num_draft=nd_of(r),
+                                     accept_len=wide(accept), scale=r.scale)
+    terms = (K + 1) * heads // 2
+    room = added * ((dim + 4) * 2.0 ** -24 * size + 2.0 ** -22 * (size + 8) + 2.0 ** -20
+                    + terms * 2.0 ** -24) + 2.0 ** -24 * ref
+    got = wide(c.weight.cpu())
+    assert (np.abs(got - ref) <= room).all()
+    assert np.array_equal(got[added == 0], ref[added == 0])
+
+
+@pytest.mark.parametrize("lens,K,heads,kv_heads,dim,page,dtype", [
+    ([500, 30], 23, 16, 4, 128, 24, "f16"), ([200, 70], 63, 8, 1, 256, 16, "bf16"), ([90], 40, 12, 2, 64, 16, "f32"),
+    ([300, 31, 32], 17, 16, 1, 256, 8, "f32"),
+])
+def test_kv_weights_of_many_rows(lens, K, heads, kv_heads, dim, page, dtype):
+    # More rows than the LDS holds at once: the chunks of a slot's sum are added one after the other.
+    print(f"\n[case] weights of many rows K={K} {heads}/{kv_heads} D={dim} {dtype}", flush=True)
+    r = make_round(lens, K, heads, kv_heads, dim, page, dtype, seed=180 + K)
+    q, k, v, table, kv = arrays(r)
+    lse = po.paged_attention(q, k, v, table, kv, scale=r.scale)[1].astype(np.float32)
+    c = cache_of(r)
+    specdec_kv_weights(dev(r.q), dev(torch.from_numpy(lse)), c, dev(r.kv_len), scale=r.scale)
+    ref, added, size = po.kv_weights(q, lse, k, table, kv, wide(r.weight), scale=r.scale)
+    # Up to `terms` stored sums of chunks, each rounded by half a step of at most the final one.
+    terms = (K + 1) * heads // kv_heads
+    room = added * ((dim + 4) * 2.0 ** -24 * size + 2.0 ** -22 * (size + 8) + 2.0 ** -20
+                    + terms * 2.0 ** -24) + 2.0 ** -24 * (1 + terms // 16) * ref
+    got = wide(c.weight.cpu())
+    assert (np.abs(got - ref) <= room).all()
+    assert np.array_equal(got[added == 0], ref[added == 0])
+
+
+# ---- eviction from caches of many slots ----
+
+def check_evict(r, lens, budget, first, last):
+    ref = po.kv_evict(wide(r.k), wide(r.v), wide(r.table), lens, wide(r.weight), wide(r.position), budget,
+                      keep_first=first, keep_last=last)
+    c = cache_of(r)
+    ws = new_kv_evict_workspace(c, budget).fill_(255)
+    got = specdec_kv_evict(c, dev(torch.tensor(lens, dtype=torch.int32)), budget, keep_first=first, keep_last=last,
+                           workspace=ws)
+    torch.cuda.synchronize()
+    for g, want in zip((c.k, c.v, c.weight, c.position, got), ref):
+        assert np.array_equal(wide(g.cpu()), want, equal_nan=g.dtype.is_floating_point)
+
+
+@pytest.mark.parametrize("lens,kv_heads,dim,page,budget,first,last,kind", [
+    ([10, 8300, 4097, 0], 2, 8, 6, 4096, 3, 100, "ties"), ([8200, 4096, 4095], 1, 8, 16, 4095, 0, 0, "spread"),
+    ([8193, 33], 1, 8, 32, 32, 4, 20, "special"), ([12288, 12289], 1, 8, 16, 12287, 0, 9, "close"),
+    ([9000, 8999], 3, 8, 5, 500, 10, 70, "equal"), ([8192, 300], 1, 8, 16, 256, 1, 1, "spread"),
+    ([700] * 80, 1, 8, 16, 300, 0, 64, "ties"),
+])
+def test_kv_evict_of_many_slots(lens, kv_heads, dim, page, budget, first, last, kind):
+    print(f"\n[case] evict {lens[:4]} page={page} budget={budget} {kind}", flush=True)
+    check_evict(evict_case(lens, kv_heads, dim, page, "bf16", seed=sum(lens), kind=kind), lens, budget, first, last)
+
+
+def test_kv_evict_of_many_slots_invalid_sequences_and_new_len_in_place():
+    lens = [8300, 100, 8250, 60, 20]
+    r = evict_case(lens, 2, 8, 16, "bf16", seed=190)
+    r.table[2, 500] = -1
+    kv = torch.tensor([8300, -1, 8250, 10 ** 9, 20], dtype=torch.int32)
+    ref = po.kv_evict(wide(r.k), wide(r.v), wide(r.table), kv.tolist(), wide(r.weight), wide(r.position), 40,
+                      keep_last=10)
+    c, n = cache_of(r), dev(kv)
+    specdec_kv_evict(c, n, 40, keep_last=10, new_len=n)
+    assert n.tolist() == [40, -1, -1, -1, 20]
+    for got, want in zip((c.k, c.v, c.weight, c.position), ref):
+        assert np.array_equal(wide(got.cpu()), want, equal_nan=got.dtype.is_floating_point)
+
+
+def test_kv_evict_new_len_beside_and_in_place_of_kv_len():
+    # A full cache gives up a few slots: the call's first kernel moves the rows itself, or where new_len is kv_len
+    # the second.
+    r = evict_case([70, 66, 64, 72], 2, 64, 8, "bf16", seed=191)
+    kv = torch.tensor([70, 66, 64, 72], dtype=torch.int32)
+    ref = po.kv_evict(wide(r.k), wide(r.v), wide(r.table), kv.tolist(), wide(r.weight), wide(r.position), 65,
+                      keep_first=2, keep_last=8)
+    for at in (0, 4):
+        both = torch.zeros(8, dtype=torch.int32, device=DEV)
+        both[:4].copy_(dev(kv))
+        c = cache_of(r)
+        specdec_kv_evict(c, both[:4], 65, keep_first=2, keep_last=8, new_len=both[at:at + 4])
+        assert both[at:at + 4].tolist() == ref[4].tolist()
+        for got, want in zip((c.k, c.v, c.weight, c.position), ref):
+            assert np.array_equal(wide(got.cpu()), want, equal_nan=got.dtype.is_floating_point)
+
+
+# ---- graphs, streams, in place ----
+
+def test_two_graphs_share_their_workspaces():
+    # Two batches captured with the same workspaces, replayed in turn between eager work.
+    rounds = [make_round([900, 40], 3, 8, 2, 64, 16, "bf16", seed=200), make_round([5, 3000], 3, 8, 2, 64, 16, "bf16",
+                                                                                   seed=201)]
+    evicts = [evict_case([8300, 100], 2, 8, 16, "bf16", seed=202), evict_case([8200, 8240], 2, 8, 16, "bf16", seed=203)]
+    caches, out, lse, graphs, lens, news = [], [], [], [], [], []
+    aws = ews = None
+    for r, e in zip(rounds, evicts):
+        c, ce = cache_of(r), cache_of(e)
+        o, l = specdec_paged_attention(dev(r.q), c, dev(r.kv_len), scale=r.scale, want_lse=True)
+        aws = new_paged_attention_workspace(c, 3, 8) if aws is None else aws
+        need = new_kv_evict_workspace(ce, 50)
+        ews = need if ews is None or need.numel() > ews.numel() else ews
+        caches.append((c, ce, [t.clone() for t in (ce.k, ce.v, ce.weight, ce.position)]))
+        out.append(o), lse.append(l), lens.append(dev(e.kv_len))
+        news.append(torch.zeros(2, dtype=torch.int32, device=DEV))
+    q, kv = [dev(r.q) for r in rounds], [dev(r.kv_len) for r in rounds]
+    torch.cuda.synchronize()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            specdec_paged_attention(q[i], caches[i][0], kv[i], scale=rounds[i].scale, out=out[i], lse=lse[i],
+                                    workspace=aws)
+            specdec_kv_evict(caches[i][1], lens[i], 50, keep_first=1, keep_last=7, new_len=news[i], workspace=ews)
+        graphs.append(g)
+    want = [po.kv_evict(wide(e.k), wide(e.v), wide(e.table), wide(e.kv_len).tolist(), wide(e.weight), wide(e.position),
+                        50, keep_first=1, keep_last=7) for e in evicts]
+    for step in range(3):
+        for i in (0, 1, 1, 0):
+            out[i].fill_(3.0)
+            for t, old in zip((caches[i][1].k, caches[i][1].v, caches[i][1].weight, caches[i][1].position),
+                              caches[i][2]):
+                t.copy_(old)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            check_attention(rounds[i], out[i], lse[i])
+            ce = caches[i][1]
+            for got, x in zip((ce.k, ce.v, ce.weight, ce.position, news[i]), want[i]):
+                assert np.array_equal(wide(got.cpu()), x, equal_nan=got.dtype.is_floating_point)
+
+
+def test_calls_at_once_on_two_streams():
+    rounds = [make_round([2000, 40], 3, 8, 2, 64, 16, "bf16", seed=210), make_round([5, 1500], 11, 8, 2, 128, 16, "f16",
+                                                                                    seed=211)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args = [(dev(r.q), cache_of(r), dev(r.kv_len)) for r in rounds]
+    alone = [specdec_paged_attention(*a, scale=r.scale, want_lse=True) for a, r in zip(args, rounds)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        both = [specdec_paged_attention(*a, scale=r.scale, want_lse=True, stream=s)
+                for a, r, s in zip(args, rounds, streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(both, alone):
+            assert same_bits(x[0], y[0]) and same_bits(x[1], y[1])
+
+
+def test_rope_in_place_with_padded_rows_and_an_empty_batch():
+    r = make_round([30, 9, 50], 4, 8, 2, 64, 16, "bf16", seed=220, ragged=True)
+    freq = dev(torch.tensor([0.5 ** i for i in range(16)], dtype=torch.float64))
+    args = (dev(r.k_new), dev(r.v_new))
+    c1, c2, q = cache_of(r), cache_of(r), dev(r.q)
+    apart = specdec_rope_append(q, *args, c1, dev(r.kv_len), freq, num_draft=dev(r.num_draft))
+    specdec_rope_append(q, *args, c2, dev(r.kv_len), freq, num_draft=dev(r.num_draft), out=q)
+    assert same_bits(q, apart) and same_bits(c1.k, c2.k) and same_bits(c1.v, c2.v)
+    none = PagedKvCache(c1.k, c1.v, c1.page_table[:0], weight=c1.weight, position=c1.position)
+    kv = torch.empty(0, dtype=torch.int32, device=DEV)
+    assert specdec_paged_attention(q[:0], none, kv)[0].shape == (0, 5, 8, 64)
+    assert specdec_kv_evict(none, kv, 5).shape == (0,)
+    specdec_kv_weights(q[:0], torch.empty(0, 5, 8, device=DEV), none, kv)
+    specdec_rope_append(q[:0], args[0][:0], args[1][:0], none, kv, freq)
+    assert same_bits(c1.k, c2.k)
