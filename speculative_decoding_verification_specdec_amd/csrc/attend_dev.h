@@ -605,12 +605,7 @@ __device__ __forceinline__ RangeStart range_start(const AttendArgs& a, const KvA
     r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
     mine += work_of<kKeys>(r, c.heads, group, plan.rows);
   }
-  long long upto = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const long long y = shfl64(upto, max(lane - off, 0));
-    if (lane >= off) upto += y;
-  }
+  const long long upto = scan_work(mine);
   RangeStart s{};
   s.total = read_lane64(upto, 63);
   // Neighbouring ranges go to one XCD (workgroups are dealt to the 8 XCDs in turn), so that row chunks of

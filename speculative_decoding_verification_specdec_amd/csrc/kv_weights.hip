@@ -178,12 +178,7 @@ __global__ __launch_bounds__(64 * kWeightWaves, kDim == 256 ? 2 : 4) void kv_wei
   const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
   long long mine = 0;
   for (int b = run0; b < run1; ++b) mine += weight_work(weight_rows<L::kKeys>(a, c, group, b), c.heads);
-  long long upto = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const long long y = shfl64(upto, max(lane - off, 0));
-    if (lane >= off) upto += y;
-  }
+  const long long upto = scan_work(mine);
   const long long total = read_lane64(upto, 63);
   // The range takes the tiles that begin in it.
   const long long begin = blockIdx.x * total >> plan.log_ranges, end = (blockIdx.x + 1LL) * total >> plan.log_ranges;

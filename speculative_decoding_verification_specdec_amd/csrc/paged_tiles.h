@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include "paged.h"
+#include "wave_ops.h"
 
 namespace specdec {
 
@@ -102,6 +103,12 @@ __device__ __forceinline__ long long read_lane64(long long x, int src) {
   const int lo = __builtin_amdgcn_readlane(static_cast<int>(x), src);
   const int hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), src);
   return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo);
+}
+
+// Inclusive sum over the lanes of whole numbers whose sums stay under 2^53: in f64 by moves between neighbouring
+// lanes, without a trip to LDS for each step.
+__device__ __forceinline__ long long scan_work(long long mine) {
+  return static_cast<long long>(wave_inclusive_scan(static_cast<double>(mine)));
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
