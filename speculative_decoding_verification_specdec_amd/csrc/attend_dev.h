@@ -589,13 +589,13 @@ __device__ __forceinline__ AttendPiece<T> make_piece(const KvArgs& c, const Atte
 // A wave's (or workgroup's) range, and the piece of a segment that it begins with.
 struct RangeStart {
   long long total, begin, end;
-  int w, b, len, n, seg, first;
+  int wg, log_waves, log_ranges, b, len, n, seg, first;
 };
 
-// Every wave finds its own: `waves` ranges a workgroup, this one's number is `wave`.
+// Every wave finds its own; its number in the workgroup is `wave` (0 where the workgroup shares one range).
 template <int kKeys>
 __device__ __forceinline__ RangeStart range_start(const AttendArgs& a, const KvArgs& c, const AttendPlan& plan,
-                                                  int group, int lane, int waves, int wave) {
+                                                  int group, int lane, int wave) {
   // Tiles before each sequence: every lane sums a run of sequences, then a scan over the lanes.
   const int per = (a.B + 63) / 64;
   const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
@@ -608,14 +608,21 @@ __device__ __forceinline__ RangeStart range_start(const AttendArgs& a, const KvA
   const long long upto = scan_work(mine);
   RangeStart s{};
   s.total = read_lane64(upto, 63);
+  // Few tiles: fewer waves of a workgroup have a range (the first ones), so that the tiles are spread over the
+  // CUs: 200 tiles of one sequence take 13.6 us on 200 of them, each part straight to memory, and 16.1 on 50.
+  const int log_groups = plan.log_ranges - plan.log_waves;
+  int log_waves = plan.log_waves;
+  while (log_waves > 0 && s.total <= 1LL << (log_groups + log_waves - 1)) --log_waves;
+  s.log_waves = log_waves;
+  s.log_ranges = log_groups + log_waves;
   // Neighbouring ranges go to one XCD (workgroups are dealt to the 8 XCDs in turn), so that row chunks of
   // the same slots meet in its L2; too few tiles for that go round all XCDs.
-  const int wg = s.total >> plan.log_ranges == 0
-                     ? static_cast<int>(blockIdx.x)
-                     : static_cast<int>(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
-  s.w = wg * waves + wave;
-  s.begin = range_begin(s.w, s.total, plan.log_ranges);
-  s.end = range_begin(s.w + 1, s.total, plan.log_ranges);
+  s.wg = s.total >> s.log_ranges == 0 ? static_cast<int>(blockIdx.x)
+                                      : static_cast<int>(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  if (wave >> log_waves) return s;
+  const int w = (s.wg << log_waves) + wave;
+  s.begin = range_begin(w, s.total, s.log_ranges);
+  s.end = range_begin(w + 1, s.total, s.log_ranges);
   if (s.begin >= s.end) return s;
   // The sequence that holds tile `begin`: the lane whose run does, then along its run.
   const int owner = __builtin_ctzll(__ballot(mine > 0 && s.begin < upto));
@@ -691,11 +698,12 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int group = a.q_heads / c.heads;
-  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, kWaves, wave);
-  const int w = at.w, wg = w / kWaves;
+  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, wave);
+  const int wg = at.wg;
   const long long begin = at.begin, end = at.end, total = at.total;
   fill_unused_rows<T>(a, c);
   if (threadIdx.x == 0) plan.cut[wg].parts = 0;
+  const bool in_lds = kWaves > 1 && at.log_waves > 0;  // (else one wave's parts are the workgroup's)
   if (kWaves > 1 && lane < 2) sh_note[2 * wave + lane].any = false;
   if (begin < end) {
   Wave s(c);
@@ -738,11 +746,11 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
     const bool begins = now.first == 0, ends = now.end == now.tiles, whole = begins && ends;
     const int h = now.seg / now.chunks, chunk = now.seg - h * now.chunks;
     const int slot = begins ? 1 : 0;
-    if (kWaves > 1 && !whole && lane == 0)
+    if (in_lds && !whole && lane == 0)
       sh_note[2 * wave + slot] = PartNote{now.b,  now.seg, now.n, now.chunks,
                                              true,   begins,  ends,  end - now.end + now.tiles};
-    if (kWaves == 1 && begins && !ends && lane == 0)
-      plan.cut[wg] = CutSegment{range_of(end - now.end + now.tiles - 1, total, plan.log_ranges) - wg + 1,
+    if (!in_lds && begins && !ends && lane == 0)
+      plan.cut[wg] = CutSegment{range_of(end - now.end + now.tiles - 1, total, at.log_ranges) - wg + 1,
                                 now.b, now.seg, now.n};
     const bool bad = __any(s.bad);
     int id = threadIdx.x & 63;  // (volatile: addresses are made here, not kept through the walk)
@@ -768,7 +776,7 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
           const f32x4 four = {s.o[t][y][x], s.o[t][y + 1][x], s.o[t][y + 2][x], s.o[t][y + 3][x]};
           if (whole) {
             if (d < c.dim) write_row<T>(a, c, row, d, four, top, sum);
-          } else if (kWaves > 1) {
+          } else if (in_lds) {
             *sh_o(2 * wave + slot, local, d) = four;
           } else {
             *reinterpret_cast<f32x4*>(plan.part_o + part_row * kDim + d) = four;
@@ -776,8 +784,13 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
           __builtin_amdgcn_sched_barrier(0);  // (few copies of the outputs at a time)
         }
       if (!whole && g == 0) {
-        (kWaves > 1 ? sh_m[2 * wave + slot][local] : plan.part_m[part_row]) = top;
-        (kWaves > 1 ? sh_l[2 * wave + slot][local] : plan.part_l[part_row]) = sum;
+        if (in_lds) {
+          sh_m[2 * wave + slot][local] = top;
+          sh_l[2 * wave + slot][local] = sum;
+        } else {
+          plan.part_m[part_row] = top;
+          plan.part_l[part_row] = sum;
+        }
       }
     }
     if (!more) break;
@@ -786,7 +799,7 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
     s.bad_next = false;
   }
   }
-  if constexpr (kWaves > 1) {
+  if (in_lds) {
     __syncthreads();
     // Neighbouring parts of one segment, in order: a wave's part that begins nothing comes first.
     for (int x = 0; x < 2 * kWaves;) {
@@ -834,7 +847,7 @@ __global__ __launch_bounds__(64 * kWaves, split_occupancy<T>(kDim, kFast, kRowTi
         }
       }
       if (first.begins && !ends && threadIdx.x == 0) {  // (it ends the workgroup's range)
-        plan.cut[wg] = CutSegment{range_of(first.segment_end - 1, total, plan.log_ranges) / kWaves - wg + 1,
+        plan.cut[wg] = CutSegment{(range_of(first.segment_end - 1, total, at.log_ranges) >> at.log_waves) - wg + 1,
                                   first.b, first.seg, first.n};
       }
       x = last + 1;
@@ -867,8 +880,8 @@ __global__ __launch_bounds__(64 * kWaves, kDim == 256 && kRowTiles == 2 ? 1 : 2)
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int group = a.q_heads / c.heads;
-  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, 1, 0);
-  const int wg = at.w;
+  const RangeStart at = range_start<L::kKeys>(a, c, plan, group, lane, 0);
+  const int wg = at.wg;
   fill_unused_rows<T>(a, c);
   if (threadIdx.x == 0) plan.cut[wg].parts = 0;
   if (at.begin >= at.end) return;
@@ -1002,7 +1015,7 @@ __global__ __launch_bounds__(64 * kWaves, kDim == 256 && kRowTiles == 2 ? 1 : 2)
     const bool begins = now.first == 0, whole = begins && now.end == now.tiles;
     const int slot = begins ? 1 : 0;
     if (begins && !whole && threadIdx.x == 0)
-      plan.cut[wg] = CutSegment{range_of(at.end - now.end + now.tiles - 1, at.total, plan.log_ranges) - wg + 1,
+      plan.cut[wg] = CutSegment{range_of(at.end - now.end + now.tiles - 1, at.total, at.log_ranges) - wg + 1,
                                 now.b, now.seg, now.n};
     const bool mine_bad = __any(s.bad);
     if (lane == 0) sh_bad[wave] = mine_bad;
