@@ -92,10 +92,12 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_append_kernel(RopeArgs a
   const int all_heads = a.q_heads + 2 * c.heads;
   for (long long w = static_cast<long long>(blockIdx.x) * kRopeWaves + (threadIdx.x >> 6);
        w < tokens * splits; w += static_cast<long long>(gridDim.x) * kRopeWaves) {
-    const long long token = w / splits;
-    const int split = static_cast<int>(w - token * splits);
-    const int b = static_cast<int>(token / (a.K + 1));
-    const int i = static_cast<int>(token - static_cast<long long>(b) * (a.K + 1));
+    // (tokens < 2^31, and there are splits only of a few thousand: 32 bits)
+    const unsigned t = static_cast<unsigned>(w) / static_cast<unsigned>(splits);
+    const int split = static_cast<int>(static_cast<unsigned>(w) - t * splits);
+    const long long token = t;
+    const int b = static_cast<int>(t / static_cast<unsigned>(a.K + 1));
+    const int i = static_cast<int>(t - static_cast<unsigned>(b) * (a.K + 1));
     const RoundRows r = round_rows(c, a.num_draft, a.kv_len, b, a.K);
     const long long pos = static_cast<long long>(a.first_pos[b]) + i;
     const int first_head = split * per_wave * per_pass;
@@ -193,7 +195,7 @@ hipError_t launch_rope_type(const RopeArgs& a, const KvArgs& c) {
   const int passes = (all_heads + per_pass - 1) / per_pass;
   const long long tokens = static_cast<long long>(a.B) * (a.K + 1);
   // Few tokens: as many waves a token as it takes to have 4096 of them (16 a CU) in flight (one token of 48 heads
-  // 6.5 us, 8.4 in one wave; 384 tokens 7.9 and 8.8).
+  // 6.5 us, 8.4 in one wave; 384 tokens 7.6 and 8.8).
   long long splits = (4096 + tokens - 1) / tokens;
   if (splits > passes) splits = passes;
   const int per_wave = static_cast<int>((passes + splits - 1) / splits);
