@@ -13,6 +13,11 @@
 namespace specdec {
 
 constexpr int kJoinThreads = 256;
+// The kernel for many rows leaves segments of so many tiles whole, with the workgroup that has their first tile: a part
+// of 64 or 128 rows costs as much as several tiles.  (64 x 100-300 slots, 64 rows on 8 heads: 35 us, 41 with all of
+// them cut; 14 x 1-9 slots, 512 rows on 8 heads, f32: 58 and 88; 64 x 500-4000 slots, 48 rows: 144 and 143, but 152
+// with segments of up to 32 tiles whole.)
+constexpr int kWholeTiles = 16;
 
 // Row chunks of a sequence with n new tokens; tiles of its slots; tiles of all its segments (none if it
 // is invalid).
@@ -504,7 +509,10 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(AttendArgs a,
   const int h = cut.seg / chunks, chunk = cut.seg - h * chunks;
   const int team = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   const int end = min(plan.rows, cut.n * group - chunk * plan.rows);
-  const bool by_part = cut.parts > kAhead;
+  // Teams share out the parts of a row or the rows, whichever takes fewer turns.
+  const int by = gridDim.y;
+  const bool by_part = (end + by - 1) / by * ((cut.parts + kAhead * kTeams - 1) / (kAhead * kTeams)) <
+                       (end + by * kTeams - 1) / (by * kTeams) * ((cut.parts + kAhead - 1) / kAhead);
   const int rows_once = by_part ? 1 : kTeams, part_step = by_part ? kTeams : 1;
   for (int row = blockIdx.y * rows_once; row < end; row += gridDim.y * rows_once) {
     const int local = by_part ? row : row + team;
@@ -569,7 +577,8 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(AttendArgs a,
 // The piece of a range that begins with tile `first` of a segment and has `left` tiles at most.
 template <typename T, int kKeys>
 __device__ __forceinline__ AttendPiece<T> make_piece(const KvArgs& c, const AttendPlan& plan, int group, int b,
-                                                     int seg, int len, int n, int first, long long left) {
+                                                     int seg, int len, int n, int first, long long left,
+                                                     int whole = 0) {
   AttendPiece<T> p;
   p.b = b;
   p.seg = seg;
@@ -578,7 +587,7 @@ __device__ __forceinline__ AttendPiece<T> make_piece(const KvArgs& c, const Atte
   p.chunks = chunks_of(n, group, plan.rows);
   p.tiles = tiles_of<kKeys>(len, n);
   p.first = first;
-  p.end = static_cast<int>(min(static_cast<long long>(p.tiles), first + left));
+  p.end = p.tiles <= whole ? p.tiles : static_cast<int>(min(static_cast<long long>(p.tiles), first + left));
   const int h = seg / p.chunks;
   p.kpool = reinterpret_cast<const T*>(c.k) + h * c.head_stride;
   p.vpool = reinterpret_cast<const T*>(c.v) + h * c.head_stride;
@@ -894,7 +903,26 @@ __global__ __launch_bounds__(64 * kWaves, kDim == 256 && kRowTiles == 2 ? 1 : 2)
   s.scale = plan.scale_log2;
   s.bad = false;
   long long left = at.end - at.begin;
-  AttendPiece<T> now = make_piece<T, L::kKeys>(c, plan, group, at.b, at.seg, at.len, at.n, at.first, left);
+  const int whole_tiles = at.total >> at.log_ranges == 0 ? 0 : kWholeTiles;  // (few tiles: one each)
+  AttendPiece<T> now =
+      make_piece<T, L::kKeys>(c, plan, group, at.b, at.seg, at.len, at.n, at.first, left, whole_tiles);
+  auto advance = [&]() __attribute__((always_inline)) {
+    int nb = now.b, seg = now.seg + 1, nlen = now.len, nn = now.n;
+    if (seg == c.heads * now.chunks) {
+      seg = 0;
+      do {
+        const RoundRows x = round_rows(c, a.num_draft, a.kv_len, ++nb, a.K);
+        nlen = uniform(x.len);
+        nn = uniform(x.n);
+      } while (nn == 0);
+    }
+    now = make_piece<T, L::kKeys>(c, plan, group, nb, seg, nlen, nn, 0, left, whole_tiles);
+  };
+  if (now.first > 0 && now.tiles <= whole_tiles) {  // (done by the workgroup that has its first tile)
+    left -= now.tiles - now.first;
+    if (left <= 0) return;
+    advance();
+  }
   const int sub = L::kSub == 2 ? 2 * wave / kWaves : 0;  // the 16-slot group of all that this wave loads
   const int step_k = wave * kMineK % L::kSteps, step_v = wave * kMineV;
 
@@ -1057,16 +1085,7 @@ __global__ __launch_bounds__(64 * kWaves, kDim == 256 && kRowTiles == 2 ? 1 : 2)
       }
     }
     if (left <= 0) return;
-    int nb = now.b, seg = now.seg + 1, nlen = now.len, nn = now.n;
-    if (seg == c.heads * now.chunks) {
-      seg = 0;
-      do {
-        const RoundRows x = round_rows(c, a.num_draft, a.kv_len, ++nb, a.K);
-        nlen = uniform(x.len);
-        nn = uniform(x.n);
-      } while (nn == 0);
-    }
-    now = make_piece<T, L::kKeys>(c, plan, group, nb, seg, nlen, nn, 0, left);
+    advance();
   }
 }
 
@@ -1089,7 +1108,9 @@ void launch_attend_dim(const AttendArgs& a, const KvArgs& c, const AttendPlan& p
       attend_split_kernel<T, kDim, kFast, 2, 4><<<groups, 256, lds, a.stream>>>(a, c, p);
   }
   const int rows = p.rows < (a.K + 1) * (a.q_heads / c.heads) ? p.rows : (a.K + 1) * (a.q_heads / c.heads);
-  attend_join_kernel<T, kDim><<<dim3(groups, rows < 8 ? rows : 8), kJoinThreads, 0, a.stream>>>(a, c, p);
+  // (the widest heads have half as many rows a workgroup; more for the others cost what they gained)
+  const int by = kDim == 256 ? 16 : 8;
+  attend_join_kernel<T, kDim><<<dim3(groups, rows < by ? rows : by), kJoinThreads, 0, a.stream>>>(a, c, p);
 }
 
 template <typename T>

@@ -23,6 +23,9 @@ MANY_ROWS = [
     ([100, 90], 20, 8, 1, 200, 10, "f32", True), ([150, 31], 12, 16, 4, 128, 16, "f32", False),
     ([150, 20], 30, 8, 2, 128, 8, "f32", True), ([90] * 70, 9, 8, 2, 64, 16, "bf16", True),
     ([40, 31, 32], 50, 3, 3, 128, 16, "bf16", True), ([30, 15, 16], 33, 4, 2, 256, 16, "f32", True),
+    # segments that are cut among segments that are left whole
+    ([900, 30] * 40, 9, 8, 2, 64, 16, "bf16", True), ([1, 700, 9, 490, 520] * 6, 16, 8, 2, 128, 24, "f16", True),
+    ([i % 10 for i in range(40)], 63, 8, 2, 64, 24, "f32", False),
 ]
 
 
