@@ -498,7 +498,7 @@ template <typename T, int kDim>
 __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(AttendArgs a, KvArgs c, AttendPlan plan) {
   constexpr int kLanes = kDim / 4;
   constexpr int kTeams = kJoinThreads / kLanes;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
   __shared__ f32x4 sh_o[kTeams][kLanes];
   __shared__ float sh_m[kTeams], sh_l[kTeams];
   const int w = blockIdx.x;

@@ -11,7 +11,7 @@
 // 64 x 16380 slots of 8 heads where plain ones take 481, 391 of them without the weights' stores; holding stores back
 // in LDS for 4-16 tiles changed that by 1%.)  The tiles of all segments, laid end to end and weighed by what they
 // cost, are cut into equal ranges, one a workgroup, whose four waves take the range's tiles in turn.
-// 64 x 500-4000 slots of 8 heads, up to 24 rows, bf16: 69.5 us, 4.4 TB/s; 4 x 50-65 k slots, up to 48 rows: 107 us.
+// 64 x 500-4000 slots of 8 heads, up to 24 rows, bf16: 69 us, 4.4 TB/s; 4 x 50-65 k slots, up to 48 rows: 105 us.
 #include <hip/hip_runtime.h>
 
 #include "paged.h"
