@@ -255,3 +255,60 @@ def test_rope_in_place_with_padded_rows_and_an_empty_batch():
     specdec_kv_weights(q[:0], torch.empty(0, 5, 8, device=DEV), none, kv)
     specdec_rope_append(q[:0], args[0][:0], args[1][:0], none, kv, freq)
     assert same_bits(c1.k, c2.k)
+
+
+# ---- far addresses ----
+
+def spread_out(r, pages, slot_first):
+    # The round's pools and records as the last pages of ones with `pages` pages; slot_first: a pool whose slots
+    # lie pages * heads * dim elements apart.
+    n, page, heads, dim = r.k.shape
+    shift = pages - n
+    pools = []
+    for t in (r.k, r.v):
+        if slot_first:
+            big = torch.zeros(page, pages, heads, dim, dtype=t.dtype, device=DEV).transpose(0, 1)
+        else:
+            big = torch.zeros(pages, page, heads, dim, dtype=t.dtype, device=DEV)
+        big[shift:] = dev(t)
+        pools.append(big)
+    records = []
+    for t in (r.weight, r.position):
+        big = torch.zeros(pages, heads, page, dtype=t.dtype, device=DEV)
+        big[shift:] = dev(t)
+        records.append(big)
+    table = torch.where((r.table >= 0) & (r.table < n), r.table + shift, r.table)
+    return PagedKvCache(*pools, dev(table), weight=records[0], position=records[1]), shift
+
+
+@pytest.mark.parametrize("pages,slot_first", [((9 << 30) // (16 * 2 * 128 * 2 * 2), False), (1 << 17, True)])
+def test_calls_on_far_addresses(pages, slot_first):
+    # Pages past 2^32 bytes from the pool's start; slots 2^25 elements apart.
+    print(f"\n[case] far addresses pages={pages} slot_first={slot_first}", flush=True)
+    r = make_round([300, 77], 3, 8, 2, 128, 16, "bf16", seed=230)
+    near, (far, shift) = cache_of(r), spread_out(r, pages, slot_first)
+    assert far.k.stride(1) >= 1 << 25 if slot_first else far.k[shift:].storage_offset() * 2 > 2 ** 32
+    freq = dev(torch.tensor([0.7 ** i for i in range(64)], dtype=torch.float64))
+    kv, results = dev(r.kv_len), []
+    for c in (near, far):
+        q = specdec_rope_append(dev(r.q), dev(r.k_new), dev(r.v_new), c, kv, freq)
+        out, lse = specdec_paged_attention(q, c, kv, want_lse=True)
+        wide_q = q.repeat(1, 12, 1, 1)[:, :40].contiguous()     # 160 rows: the kernel for many rows
+        many, _ = specdec_paged_attention(wide_q, c, kv - 36)
+        specdec_kv_weights(q, lse, c, kv)
+        n = specdec_kv_evict(c, kv + 4, 70, keep_first=2, keep_last=9)
+        torch.cuda.synchronize()
+        results.append([q, out, lse, many, n] + [t[-r.k.shape[0]:] for t in (c.k, c.v, c.weight, c.position)])
+    # What is only moved or turned is the same.  The attention of either stride rule is within two half steps of bf16
+    # (2^-8 each) of the formula, so within 2^-6 of the other; lse within 2 (e_x + 2^-18) < 1e-5; a weight's terms by
+    # as much in their exponents (scores and lse): 1e-4 with its sum.
+    for i, (x, y) in enumerate(zip(*results)):
+        if i in (1, 3):
+            assert torch.allclose(x.float(), y.float(), rtol=2.0 ** -6, atol=2.0 ** -6, equal_nan=True)
+        elif i == 2:
+            assert torch.allclose(x, y, rtol=1e-5, atol=1e-5)
+        elif i == 7:
+            assert torch.allclose(x, y, rtol=1e-4)
+        elif i != 5 and i != 6 or not slot_first:
+            assert same_bits(x, y)
+    assert torch.isfinite(results[1][1]).all()
